@@ -295,6 +295,164 @@ pa_status pa_decode_gqa(void* out, pa_dtype out_dt, const void* q, const void* k
                         int B, int H, int Hkv, int D, int S, int NB, pa_dtype dt, int partition,
                         int max_seq_len, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions (not on the pages, whose keys and queries arrive rotated):
+ * for each token t and head, of a row x of D elements
+ *   norm     x / sqrt(mean(x^2) + eps) * weight, where a weight is given (one
+ *            weight [D] for all query heads, one for all key heads)
+ *   rotation of its first rot_dim elements: pair j (elements j and
+ *            j + rot_dim / 2, or 2j and 2j + 1 when interleaved != 0) turned by
+ *            the angle 2 pi * frac(positions[t] * table[j]), both components
+ *            multiplied by `amplitude`; the other elements pass through.
+ * All of it in fp32 (the angle's turns in 64 bits, so far positions lose
+ * nothing), rounded once to the output type.
+ *
+ * pa_rope_table (host) fills table [rot_dim / 2] (64 bits, HOST memory: the
+ * caller copies it to the device once) with turns per position,
+ * f_j / (2 pi), f_j = base^(-2 j / rot_dim), changed by `scaling`:
+ *   PA_ROPE_PLAIN   as is
+ *   PA_ROPE_LINEAR  f_j / factor
+ *   PA_ROPE_NTK     base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   PA_ROPE_YARN    f_j / factor where a pair makes fewer than `low` turns over
+ *                   original_len positions, f_j where it makes more than
+ *                   `high`, linear in j between; *amplitude = 0.1 ln(factor) + 1
+ *   PA_ROPE_BANDS   f_j / factor where the wavelength 2 pi / f_j exceeds
+ *                   original_len / low, f_j where it is below
+ *                   original_len / high, linear in original_len / wavelength
+ *                   between
+ * *amplitude receives 1 otherwise. rot_dim even and > 0 (> 2 for NTK), base > 1,
+ * factor >= 1; for YARN and BANDS 0 < low < high and original_len > 0.
+ * A caller with frequencies of its own fills the table itself.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+  PA_ROPE_PLAIN = 0,
+  PA_ROPE_LINEAR = 1,
+  PA_ROPE_NTK = 2,
+  PA_ROPE_YARN = 3,
+  PA_ROPE_BANDS = 4
+} pa_rope_scaling;
+
+pa_status pa_rope_table(double* table, int rot_dim, double base, pa_rope_scaling scaling,
+                        double factor, double low, double high, double original_len,
+                        float* amplitude);
+
+/* Norm and rotation of queries and keys.
+ *   q, k          [T, H, D], [T, Hkv, D], dtype dt; token t's rows start
+ *                 q_stride / k_stride elements after token t - 1's (so the parts
+ *                 of a fused projection's output can be given in place), heads
+ *                 contiguous
+ *   q_out, k_out  the same shapes with strides of their own; q_out may be q and
+ *                 k_out may be k (same stride); other overlaps are undefined
+ *   positions     [T] int32 device
+ *   table         [rot_dim / 2] 64-bit floats, device
+ *   q_weight, k_weight  [D] dtype dt, or NULL for no norm of that part; 16-byte
+ *                 aligned
+ * H or Hkv may be 0 (that part's pointers are then not looked at). D a multiple
+ * of 8, at most 256; rot_dim even, 2 .. D; strides multiples of 8 elements
+ * and at least heads * D; 16-byte aligned q, k, q_out, k_out; table 8-byte
+ * aligned. eps finite and >= 0, amplitude finite. T == 0 is a no-op. */
+pa_status pa_rope(void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                  const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                  const int32_t* positions, const double* table, int rot_dim, int interleaved,
+                  float amplitude, const void* q_weight, const void* k_weight, float eps, int T,
+                  int H, int Hkv, int D, pa_dtype dt, void* stream);
+
+/* The same with the append: k's normed and rotated rows and v's rows ([T, Hkv, D],
+ * v_stride) go to k_cache, v_cache [NB, Hkv, S, D] at slot_mapping as in
+ * pa_kv_append (negative slots skip a token's k and v, its q_out is written all
+ * the same; slots at or past NB * S are skipped and flagged PA_DEVERR_SLOT;
+ * slots must be distinct). v is copied bit for bit. The result is pa_rope's
+ * followed by pa_kv_append's, bit for bit, in one pass over the data. Hkv >= 1;
+ * H may be 0. Caches 16-byte aligned. */
+pa_status pa_rope_append(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         const int32_t* positions, const int64_t* slot_mapping, void* k_cache,
+                         void* v_cache, const double* table, int rot_dim, int interleaved,
+                         float amplitude, const void* q_weight, const void* k_weight, float eps,
+                         int T, int H, int Hkv, int D, int S, int NB, pa_dtype dt, void* stream);
+
+/* The same into E4M3 caches (as pa_kv_append_fp8): k's rows are stored as the
+ * codes of fp32(value / k_scale) of the 32-bit normed and rotated values (not
+ * rounded to dt on the way), v's as pa_kv_append_fp8 stores them. D a
+ * multiple of 16; scales finite and > 0. */
+pa_status pa_rope_append_fp8(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const int32_t* positions, const int64_t* slot_mapping, void* k_cache,
+                             void* v_cache, float k_scale, float v_scale, const double* table,
+                             int rot_dim, int interleaved, float amplitude, const void* q_weight,
+                             const void* k_weight, float eps, int T, int H, int Hkv, int D, int S,
+                             int NB, pa_dtype dt, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Cross attention to cached states of another length (an encoder's, for
+ * example; not on the pages): request i's keys and values are the first
+ * kv_lens[i] tokens of its blocks, its queries the rows q_start[i] ..
+ * q_start[i+1] - 1, and every query sees every one of those tokens:
+ *   out[r, h] = softmax_t(scale * q[r, h] . K_t) V_t,  t < kv_lens[i],
+ * query head h reading KV head h / (H / Hkv). kv_lens[i] == 0 gives all-zero
+ * rows. q, out, caches, tables, q_start, T and max_q_len as in pa_prefill;
+ * rows of q outside q_start[0] .. q_start[B] are left as they were. Few query
+ * rows over long states are split over the keys and merged by log-sum-exp:
+ *   max_kv_len    host bound on kv_lens, at most MB * S (longer ones are clamped
+ *                 to it and flagged PA_DEVERR_SEQ_LEN)
+ *   partition     0 = choose automatically, -1 = never split, > 0 = partitions
+ *                 of this many tokens (a multiple of 128)
+ *   workspace     as in pa_decode, pa_cross_workspace_bytes(...) for the same
+ *                 arguments
+ * D 64, 128 or 256; S one of 8, 16, 32, 64, 128; H / Hkv at most 128;
+ * NB * Hkv * S <= 2^31 - 1; B <= 65535; scale finite and > 0. Errors as in pa_prefill
+ * (a request whose q_start is inconsistent is skipped and flagged; kv_lens below
+ * 0 count as 0 and are flagged).
+ * ------------------------------------------------------------------------- */
+size_t pa_cross_workspace_bytes(int B, int T, int H, int Hkv, int D, int max_q_len, int max_kv_len,
+                                int partition);
+
+pa_status pa_cross(void* out, pa_dtype out_dt, const void* q, const void* k_cache,
+                   const void* v_cache, const int32_t* block_tables, int MB,
+                   const int32_t* kv_lens, const int32_t* q_start, float scale, int B, int H,
+                   int Hkv, int D, int S, int NB, pa_dtype dt, int T, int max_q_len,
+                   int max_kv_len, int partition, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Decode for batches that share prefixes ([vllm] Step 9 "Safe Sharing with
+ * Copy-on-Write": sequences forked from one another name the same physical
+ * blocks). The result is pa_decode_gqa's for the same q, caches, block_tables
+ * and seq_lens (no append), but the tokens that a group of requests share are
+ * read once for the whole group:
+ *   group_start   [NG + 1] int32 device: group j is the requests group_start[j]
+ *                 .. group_start[j+1] - 1; group_start[0] = 0, non-decreasing,
+ *                 group_start[NG] = B (a request that shares nothing is a group of
+ *                 one)
+ *   shared_lens   [B] int32 device: the first shared_lens[b] tokens of request b
+ *                 lie in physical blocks that the tables of all requests of
+ *                 its group name alike (pa_seq_fork makes such tables); the same
+ *                 number throughout a group. Only whole blocks inside the
+ *                 request's length are taken from the group
+ *                 (min(shared_lens[b], seq_lens[b]) rounded down to S); the rest, the
+ *                 request's tail, is read through its own table
+ *   max_group, max_shared_len, max_tail_len   host bounds on a group's requests,
+ *                 on shared_lens, and on seq_lens[b] minus the shared part (a
+ *                 longer tail is clamped and flagged PA_DEVERR_SEQ_LEN)
+ *   workspace     pa_decode_shared_workspace_bytes(...) for the same arguments, as
+ *                 in pa_decode
+ * seq_lens[b] == 0 gives an all-zero row; a negative length, a shared length
+ * outside [0, max_shared_len] and a group outside [0, B] or of more than
+ * max_group requests are flagged PA_DEVERR_SEQ_LEN, with undefined output rows.
+ * A request shorter than its group's shared part is exact as long as the V
+ * values of the group's shared tokens are finite. D 64, 128 or 256; S 8, 16 or
+ * 32; H / Hkv at most 128; B, NG <= 65535; NB * Hkv * S <= 2^31 - 1; scale finite
+ * and > 0; 16-byte aligned q, out, caches and workspace.
+ * ------------------------------------------------------------------------- */
+size_t pa_decode_shared_workspace_bytes(int B, int NG, int H, int Hkv, int D, int S, int max_group,
+                                        int max_shared_len, int max_tail_len);
+
+pa_status pa_decode_shared(void* out, pa_dtype out_dt, const void* q, const void* k_cache,
+                           const void* v_cache, const int32_t* block_tables, int MB,
+                           const int32_t* seq_lens, const int32_t* shared_lens,
+                           const int32_t* group_start, int NG, float scale, int B, int H, int Hkv,
+                           int D, int S, int NB, pa_dtype dt, int max_group, int max_shared_len,
+                           int max_tail_len, void* workspace, size_t ws_bytes, void* stream);
+
 /* Split-KV workspace layout, for tests that inspect the partition pass
  * (NP = number of partitions, n = B*H*NP, all fp32, offsets in bytes from
  * `workspace`):

@@ -59,6 +59,37 @@ _SIGNATURES = {
     # B, H, Hkv, D, S, NB, dt, T, max_q_len, stream
     "pa_prefill": ([_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, ctypes.c_float, _i32, _i32,
                     _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
+    # table, rot_dim, base, scaling, factor, low, high, original_len, amplitude
+    "pa_rope_table": ([_vp, _i32, ctypes.c_double, _i32, ctypes.c_double, ctypes.c_double,
+                       ctypes.c_double, ctypes.c_double, _vp], _i32),
+    # q_out, its stride, k_out, its stride, q, stride, k, stride, positions, table, rot_dim,
+    # interleaved, amplitude, q_weight, k_weight, eps, T, H, Hkv, D, dt, stream
+    "pa_rope": ([_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, ctypes.c_float,
+                 _vp, _vp, ctypes.c_float, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
+    # q_out, stride, q, stride, k, stride, v, stride, positions, slot_mapping, k_cache, v_cache,
+    # (fp8: k_scale, v_scale,) table, rot_dim, interleaved, amplitude, q_weight, k_weight, eps,
+    # T, H, Hkv, D, S, NB, dt, stream
+    "pa_rope_append": ([_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32,
+                        _i32, ctypes.c_float, _vp, _vp, ctypes.c_float, _i32, _i32, _i32, _i32,
+                        _i32, _i32, _i32, _vp], _i32),
+    "pa_rope_append_fp8": ([_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
+                            ctypes.c_float, ctypes.c_float, _vp, _i32, _i32, ctypes.c_float, _vp,
+                            _vp, ctypes.c_float, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp],
+                           _i32),
+    # B, T, H, Hkv, D, max_q_len, max_kv_len, partition
+    "pa_cross_workspace_bytes": ([_i32] * 8, _sz),
+    # out, out_dt, q, k_cache, v_cache, block_tables, MB, kv_lens, q_start, scale, B, H, Hkv, D,
+    # S, NB, dt, T, max_q_len, max_kv_len, partition, workspace, ws_bytes, stream
+    "pa_cross": ([_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, ctypes.c_float, _i32, _i32, _i32,
+                  _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _sz, _vp], _i32),
+    # B, NG, H, Hkv, D, S, max_group, max_shared_len, max_tail_len
+    "pa_decode_shared_workspace_bytes": ([_i32] * 9, _sz),
+    # out, out_dt, q, k_cache, v_cache, block_tables, MB, seq_lens, shared_lens, group_start, NG,
+    # scale, B, H, Hkv, D, S, NB, dt, max_group, max_shared_len, max_tail_len, workspace,
+    # ws_bytes, stream
+    "pa_decode_shared": ([_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32,
+                          ctypes.c_float, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                          _i32, _vp, _sz, _vp], _i32),
     "pa_stepper_create": ([_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                            ctypes.c_float, _i32, _i32, _i32, _i32, _vp, _vp], _i32),
     "pa_stepper_destroy": ([_vp], None),
@@ -408,6 +439,248 @@ def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_lens, scale, m
 def pa_noalloc_scratch_bytes():
     """Size of the library's static scratch array that pa_decode_noalloc uses."""
     return int(lib().pa_noalloc_scratch_bytes())
+
+
+# ---- rotary positions, cross attention, shared prefixes ----------------------------
+
+PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN, PA_ROPE_BANDS = range(5)
+
+
+class _Here:
+    """The guard of a call whose tensors are on the current device."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE_GUARD = _Here()
+
+
+def _on_device(named):
+    """Checks that the tensors are CUDA tensors of one device and returns a guard under which that
+    device is current (the call's stream defaults to its current stream)."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the others on {dev}")
+    return _HERE_GUARD if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _contiguous(named):
+    for name, t in named:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _of_type(named, dtype):
+    for name, t in named:
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}".replace("torch.", ""))
+
+
+def _half_type(t, name):
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{name} must be float16 or bfloat16")
+    return t.dtype
+
+
+def _token_stride(t, name):
+    """Elements from one token's rows to the next's of t [T, heads, D], heads contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, D]")
+    if t.numel() == 0:
+        return t.shape[1] * t.shape[2]
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    # (one token has no next one)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def pa_rope_table(rot_dim, base=10000.0, scaling=PA_ROPE_PLAIN, factor=1.0, low=1.0, high=32.0,
+                  original_len=0.0):
+    """(table, amplitude): turns per position of each of rot_dim / 2 pairs, a CPU float64 tensor
+    to be copied to the device once, and the factor on both components of a pair. scaling: one
+    of PA_ROPE_PLAIN, _LINEAR, _NTK, _YARN, _BANDS (low, high: turns over original_len)."""
+    table = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float64)
+    amplitude = ctypes.c_float()
+    _check(lib().pa_rope_table(_ptr(table), int(rot_dim), float(base), int(scaling),
+                               float(factor), float(low), float(high), float(original_len),
+                               ctypes.byref(amplitude)), "pa_rope_table")
+    return table, amplitude.value
+
+
+def _rope_common(q, k, positions, table, q_weight, k_weight, more):
+    """Checks shared by the pa_rope calls; returns (guard, T, H, Hkv, D)."""
+    guard = _on_device((("q", q), ("k", k), ("positions", positions), ("table", table),
+                        ("q_weight", q_weight), ("k_weight", k_weight)) + more)
+    dt = _half_type(q, "q")
+    _of_type((("k", k), ("q_weight", q_weight), ("k_weight", k_weight)), dt)
+    _of_type((("positions", positions),), torch.int32)
+    _of_type((("table", table),), torch.float64)
+    _contiguous((("positions", positions), ("table", table), ("q_weight", q_weight),
+                 ("k_weight", k_weight)))
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError("q must be [T, H, D] and k [T, Hkv, D]")
+    T, H, D = q.shape
+    if positions.shape != (T,) or table.dim() != 1:
+        raise ValueError("positions must be [T] and table [rot_dim / 2]")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and w.shape != (D,):
+            raise ValueError(f"{name} must be [D]")
+    return guard, T, H, k.shape[1], D
+
+
+def pa_rope(q_out, k_out, q, k, positions, table, interleaved=False, amplitude=1.0, q_weight=None,
+            k_weight=None, eps=1e-6, stream=None):
+    """Norms (where a weight [D] is given) and rotates q [T, H, D] and k [T, Hkv, D] at
+    positions [T] (int32) into q_out, k_out (which may be q, k). Tokens may be strided, heads are
+    contiguous; table: float64 [rot_dim / 2] on the device (pa_rope_table)."""
+    guard, T, H, Hkv, D = _rope_common(q, k, positions, table, q_weight, k_weight,
+                                       (("q_out", q_out), ("k_out", k_out)))
+    _of_type((("q_out", q_out), ("k_out", k_out)), q.dtype)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    with guard:
+        _check(lib().pa_rope(
+            _ptr(q_out), _token_stride(q_out, "q_out"), _ptr(k_out), _token_stride(k_out, "k_out"),
+            _ptr(q), _token_stride(q, "q"), _ptr(k), _token_stride(k, "k"), _ptr(positions),
+            _ptr(table), 2 * table.numel(), int(bool(interleaved)), float(amplitude),
+            _ptr(q_weight), _ptr(k_weight), float(eps), T, H, Hkv, D, _DT[q.dtype],
+            _stream(stream)), "pa_rope")
+
+
+def _rope_append(name, q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, scales, table,
+                 interleaved, amplitude, q_weight, k_weight, eps, stream):
+    guard, T, H, Hkv, D = _rope_common(
+        q, k, positions, table, q_weight, k_weight,
+        (("q_out", q_out), ("v", v), ("slot_mapping", slot_mapping), ("k_cache", k_cache),
+         ("v_cache", v_cache)))
+    _of_type((("q_out", q_out), ("v", v)), q.dtype)
+    _of_type((("slot_mapping", slot_mapping),), torch.int64)
+    if scales:
+        if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
+            raise ValueError("E4M3 caches are uint8 tensors of codes")
+    else:
+        _of_type((("k_cache", k_cache), ("v_cache", v_cache)), q.dtype)
+    _contiguous((("slot_mapping", slot_mapping), ("k_cache", k_cache), ("v_cache", v_cache)))
+    if q_out.shape != q.shape or v.shape != k.shape or slot_mapping.shape != (T,):
+        raise ValueError("q_out must have q's shape, v k's, and slot_mapping must be [T]")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[1] != Hkv \
+            or k_cache.shape[3] != D:
+        raise ValueError("the caches must be [NB, Hkv, S, D]")
+    NB, _, S, _ = k_cache.shape
+    with guard:
+        _check(getattr(lib(), name)(
+            _ptr(q_out), _token_stride(q_out, "q_out"), _ptr(q), _token_stride(q, "q"), _ptr(k),
+            _token_stride(k, "k"), _ptr(v), _token_stride(v, "v"), _ptr(positions),
+            _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(table),
+            2 * table.numel(), int(bool(interleaved)), float(amplitude), _ptr(q_weight),
+            _ptr(k_weight), float(eps), T, H, Hkv, D, S, NB, _DT[q.dtype], _stream(stream)), name)
+
+
+def pa_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, table,
+                   interleaved=False, amplitude=1.0, q_weight=None, k_weight=None, eps=1e-6,
+                   stream=None):
+    """pa_rope of q into q_out and of k into k_cache, with v into v_cache, at slot_mapping [T]
+    (int64; negative slots skip a token's k and v): one pass instead of pa_rope and pa_kv_append,
+    the same bits."""
+    _rope_append("pa_rope_append", q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, (),
+                 table, interleaved, amplitude, q_weight, k_weight, eps, stream)
+
+
+def pa_rope_append_fp8(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                       table, interleaved=False, amplitude=1.0, q_weight=None, k_weight=None,
+                       eps=1e-6, stream=None):
+    """pa_rope_append into uint8 E4M3 caches: codes of fp32(value / scale)."""
+    _rope_append("pa_rope_append_fp8", q_out, q, k, v, positions, slot_mapping, k_cache, v_cache,
+                 (float(k_scale), float(v_scale)), table, interleaved, amplitude, q_weight,
+                 k_weight, eps, stream)
+
+
+def _paged_common(out, q, k_cache, v_cache, block_tables, int32s, workspace):
+    """Checks shared by pa_cross and pa_decode_shared; returns the device guard."""
+    named = (("out", out), ("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
+             ("block_tables", block_tables)) + int32s
+    guard = _on_device(named + (("workspace", workspace),))
+    _contiguous(named + (("workspace", workspace),))
+    dt = _half_type(q, "q")
+    _of_type((("k_cache", k_cache), ("v_cache", v_cache)), dt)
+    _of_type((("block_tables", block_tables),) + int32s, torch.int32)
+    if out.dtype not in _DT:
+        raise ValueError("out must be float32, float16 or bfloat16")
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q and out must be [rows, H, D]")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != q.shape[2]:
+        raise ValueError("the caches must be [NB, Hkv, S, D]")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [B, MB]")
+    return guard
+
+
+def _ws_bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def pa_cross_workspace_bytes(B, T, H, Hkv, D, max_q_len, max_kv_len, partition=0):
+    return int(lib().pa_cross_workspace_bytes(B, T, H, Hkv, D, max_q_len, max_kv_len, partition))
+
+
+def pa_cross(out, q, k_cache, v_cache, block_tables, kv_lens, q_start, scale, max_q_len,
+             max_kv_len, partition=0, workspace=None, stream=None):
+    """Cross attention over cached states: rows q_start[i] .. q_start[i + 1] - 1 of q [T, H, D]
+    each see all kv_lens[i] tokens of block_tables[i]; caches [NB, Hkv, S, D]. workspace: a
+    CUDA uint8 tensor of pa_cross_workspace_bytes(...) bytes, or None when that is 0."""
+    guard = _paged_common(out, q, k_cache, v_cache, block_tables,
+                          (("kv_lens", kv_lens), ("q_start", q_start)), workspace)
+    T, H, D = q.shape
+    NB, Hkv, S, _ = k_cache.shape
+    B, MB = block_tables.shape
+    if kv_lens.shape != (B,) or q_start.shape != (B + 1,):
+        raise ValueError("kv_lens must be [B] and q_start [B + 1]")
+    with guard:
+        _check(lib().pa_cross(_ptr(out), _DT[out.dtype], _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                              _ptr(block_tables), MB, _ptr(kv_lens), _ptr(q_start), float(scale),
+                              B, H, Hkv, D, S, NB, _DT[q.dtype], T, int(max_q_len),
+                              int(max_kv_len), int(partition), _ptr(workspace),
+                              _ws_bytes(workspace), _stream(stream)), "pa_cross")
+
+
+def pa_decode_shared_workspace_bytes(B, NG, H, Hkv, D, S, max_group, max_shared_len,
+                                     max_tail_len):
+    return int(lib().pa_decode_shared_workspace_bytes(B, NG, H, Hkv, D, S, max_group,
+                                                      max_shared_len, max_tail_len))
+
+
+def pa_decode_shared(out, q, k_cache, v_cache, block_tables, seq_lens, shared_lens, group_start,
+                     scale, max_group, max_shared_len, max_tail_len, workspace=None, stream=None):
+    """pa_decode_gqa's result for q, out [B, H, D] and caches [NB, Hkv, S, D], the first
+    shared_lens[b] tokens of the requests of a group (group_start [NG + 1]) read once for the
+    group. workspace: a CUDA uint8 tensor of pa_decode_shared_workspace_bytes(...) bytes."""
+    guard = _paged_common(out, q, k_cache, v_cache, block_tables,
+                          (("seq_lens", seq_lens), ("shared_lens", shared_lens),
+                           ("group_start", group_start)), workspace)
+    B, H, D = q.shape
+    NB, Hkv, S, _ = k_cache.shape
+    if block_tables.shape[0] != B or seq_lens.shape != (B,) or shared_lens.shape != (B,) \
+            or group_start.dim() != 1 or group_start.shape[0] < 1:
+        raise ValueError("block_tables must be [B, MB], seq_lens and shared_lens [B], "
+                         "group_start [NG + 1]")
+    with guard:
+        _check(lib().pa_decode_shared(
+            _ptr(out), _DT[out.dtype], _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+            block_tables.shape[1], _ptr(seq_lens), _ptr(shared_lens), _ptr(group_start),
+            group_start.shape[0] - 1, float(scale), B, H, Hkv, D, S, NB, _DT[q.dtype],
+            int(max_group), int(max_shared_len), int(max_tail_len), _ptr(workspace),
+            _ws_bytes(workspace), _stream(stream)), "pa_decode_shared")
 
 
 def pa_copy_blocks(k_cache, v_cache, src_dst, stream=None):

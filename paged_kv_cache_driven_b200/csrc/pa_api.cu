@@ -38,16 +38,7 @@ bool decode_shape_ok(int D, int S) {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// SMs of the current device (148 on B200; also the answer without a device).
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-    cudaGetLastError();  // clear the error state of the failed query
-    return 148;
-  }
-  return n;
-}
+using pa::host::sm_count;
 
 // Chooses the partition length. Returns false on an invalid `partition`.
 //   -1      never split: one partition covering any length up to MB * S
@@ -218,9 +209,40 @@ struct RowMapKey {
 namespace pa {
 namespace host {
 
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();  // clear the error state of the failed query
+    return 148;
+  }
+  return n;
+}
+
 // kind: 0 = f16, 1 = bf16: boxes of 64 elements, so every box row is 128 bytes,
 // the 128-byte swizzle's width; 2 = one-byte E4M3 codes: a box spans the whole
 // D-byte row, unswizzled (the consumer converts it to 16-bit tiles itself).
+static bool encode_row_map(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows,
+                           int kind) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const bool codes = kind == 2;
+  const cuuint64_t esize = codes ? 1 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * esize};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(codes ? D : 128 / esize),
+                             static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType type =
+      codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+            : (kind == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+  return fn(out, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static bool row_map_kind(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows,
                          int kind) {
   static std::mutex mu;
@@ -234,24 +256,8 @@ static bool row_map_kind(CUtensorMap* out, const void* base, int64_t rows, int D
       *out = maps[k];
       return true;
     }
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const bool codes = kind == 2;
-  const cuuint64_t esize = codes ? 1 : 2;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * esize};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(codes ? D : 128 / esize),
-                             static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType type =
-      codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-            : (kind == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
   CUtensorMap map;
-  if (fn(&map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE,
-         codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
+  if (!encode_row_map(&map, base, rows, D, box_rows, kind)) return false;
   const int slot = used < 16 ? used++ : next;
   next = (slot + 1) % 16;
   keys[slot] = key;
@@ -262,6 +268,27 @@ static bool row_map_kind(CUtensorMap* out, const void* base, int64_t rows, int D
 
 bool row_map(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows, pa_dtype dt) {
   return row_map_kind(out, base, rows, D, box_rows, dt == PA_BF16 ? 1 : 0);
+}
+
+bool query_rows_map(CUtensorMap* out, const void* q, int64_t T, int H, int D, int heads, int rows,
+                    pa_dtype dt) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+                              static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
+                                 static_cast<cuuint64_t>(H) * D * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(out, dt == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            3, const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool row_map_now(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows,
+                 pa_dtype dt) {
+  return encode_row_map(out, base, rows, D, box_rows, dt == PA_BF16 ? 1 : 0);
 }
 
 bool row_map_codes(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows) {
@@ -633,7 +660,8 @@ pa_status pa_get_device_error(void* stream, uint32_t* flags) {
   unsigned int v = 0;
   using namespace pa::host;
   if (!take_error_append(&v) || !take_error_decode16(&v) || !take_error_grouped(&v) ||
-      !take_error_fp8(&v) || !take_error_prefill(&v))
+      !take_error_fp8(&v) || !take_error_prefill(&v) || !take_error_rope(&v) ||
+      !take_error_rows(&v) || !take_error_shared(&v))
     return PA_ERR_CUDA;
   *flags = v;
   return PA_OK;
@@ -727,3 +755,437 @@ extern "C" pa_status pa_decode_noalloc(void* out, pa_dtype out_dt, const void* q
   return pa_decode(out, out_dt, q, k_cache, v_cache, block_tables, MB, seq_lens, scale, B, H, D, S,
                    NB, dt, partition, max_seq_len, scratch, PA_NOALLOC_SCRATCH_BYTES, stream);
 }
+
+// ---------------------------------------------------------------------------
+// pa_rope, pa_rope_append, pa_rope_append_fp8
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// The checks that the three share (Hkv rows of k; v and the caches apart).
+bool rope_args_ok(const pa::RopeParams& prm, pa_dtype dt) {
+  if (prm.T < 0 || prm.H < 0 || prm.Hkv < 0 || !cache_dtype_ok(dt)) return false;
+  if (prm.D <= 0 || prm.D % 8 != 0 || prm.D > 256) return false;
+  if (prm.rot < 2 || prm.rot % 2 != 0 || prm.rot > prm.D) return false;
+  if (!std::isfinite(prm.amplitude) || !(std::isfinite(prm.eps) && prm.eps >= 0.f)) return false;
+  const int64_t q_row = static_cast<int64_t>(prm.H) * prm.D;
+  const int64_t k_row = static_cast<int64_t>(prm.Hkv) * prm.D;
+  return q_row <= INT_MAX / 2 && k_row <= INT_MAX / 4;
+}
+
+bool rows_ok(const void* p, int64_t stride, int heads, int D) {
+  return p && aligned16(p) && stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * D;
+}
+
+bool rope_pointers_ok(const pa::RopeParams& prm) {
+  if (!prm.positions || !prm.table || (reinterpret_cast<uintptr_t>(prm.table) & 7u)) return false;
+  if (prm.H > 0 && (!rows_ok(prm.q, prm.q_stride, prm.H, prm.D) ||
+                    !rows_ok(prm.q_out, prm.q_out_stride, prm.H, prm.D)))
+    return false;
+  if (prm.Hkv > 0 && !rows_ok(prm.k, prm.k_stride, prm.Hkv, prm.D)) return false;
+  return (!prm.q_weight || aligned16(prm.q_weight)) && (!prm.k_weight || aligned16(prm.k_weight));
+}
+
+pa::RopeParams rope_params(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                           const void* k, int64_t k_stride, const int32_t* positions,
+                           const double* table, int rot_dim, float amplitude,
+                           const void* q_weight, const void* k_weight, float eps, int T, int H,
+                           int Hkv, int D) {
+  pa::RopeParams prm{};
+  prm.q_out = q_out;
+  prm.q_out_stride = q_out_stride;
+  prm.q = q;
+  prm.q_stride = q_stride;
+  prm.k = k;
+  prm.k_stride = k_stride;
+  prm.positions = positions;
+  prm.table = table;
+  prm.rot = rot_dim;
+  prm.amplitude = amplitude;
+  prm.q_weight = H > 0 ? q_weight : nullptr;
+  prm.k_weight = Hkv > 0 ? k_weight : nullptr;
+  prm.eps = eps;
+  prm.T = T;
+  prm.H = H;
+  prm.Hkv = Hkv;
+  prm.D = D;
+  prm.rows = H + Hkv;
+  return prm;
+}
+
+// The append forms' part, and the launch.
+pa_status rope_append(pa::RopeParams& prm, const void* v, int64_t v_stride,
+                      const int64_t* slot_mapping, void* k_cache, void* v_cache, int S, int NB,
+                      pa_dtype dt, int interleaved, int mode, void* stream) {
+  if (!rope_args_ok(prm, dt) || prm.Hkv <= 0 || S <= 0 || NB < 0) return PA_ERR_INVALID;
+  if (prm.T == 0) return PA_OK;
+  if (!rope_pointers_ok(prm) || !rows_ok(v, v_stride, prm.Hkv, prm.D)) return PA_ERR_INVALID;
+  if (!slot_mapping || !k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache))
+    return PA_ERR_INVALID;
+  prm.v = v;
+  prm.v_stride = v_stride;
+  prm.slots = slot_mapping;
+  prm.k_cache = k_cache;
+  prm.v_cache = v_cache;
+  prm.S = S;
+  prm.n_slots = static_cast<int64_t>(NB) * S;
+  prm.rows = prm.H + 2 * prm.Hkv;
+  return pa::host::launch_rope(prm, dt, interleaved, mode, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_rope_table(double* table, int rot_dim, double base, pa_rope_scaling scaling,
+                        double factor, double low, double high, double original_len,
+                        float* amplitude) {
+  constexpr double kTwoPi = 6.283185307179586476925;
+  if (!table || !amplitude || rot_dim < 2 || rot_dim % 2 != 0) return PA_ERR_INVALID;
+  if (!(std::isfinite(base) && base > 1.0)) return PA_ERR_INVALID;
+  if (scaling < PA_ROPE_PLAIN || scaling > PA_ROPE_BANDS) return PA_ERR_INVALID;
+  if (scaling != PA_ROPE_PLAIN && !(std::isfinite(factor) && factor >= 1.0)) return PA_ERR_INVALID;
+  if (scaling == PA_ROPE_NTK && rot_dim == 2) return PA_ERR_INVALID;
+  const bool ranged = scaling == PA_ROPE_YARN || scaling == PA_ROPE_BANDS;
+  if (ranged && !(std::isfinite(high) && std::isfinite(original_len) && low > 0.0 && high > low &&
+                  original_len > 0.0))
+    return PA_ERR_INVALID;
+  if (scaling == PA_ROPE_NTK)
+    base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+  // YaRN: the pair index that makes r turns over original_len positions
+  auto pair_of = [&](double r) {
+    return rot_dim * std::log(original_len / (r * kTwoPi)) / (2.0 * std::log(base));
+  };
+  double first = 0.0, last = 0.0;  // pairs up to `first` keep f_j, from `last` on f_j / factor
+  if (scaling == PA_ROPE_YARN) {
+    first = std::max(std::floor(pair_of(high)), 0.0);
+    last = std::min(std::ceil(pair_of(low)), rot_dim - 1.0);
+    if (last <= first) last = first + 1e-3;
+  }
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    double f = std::pow(base, -2.0 * j / rot_dim);
+    if (scaling == PA_ROPE_LINEAR) {
+      f /= factor;
+    } else if (scaling == PA_ROPE_YARN) {
+      const double ramp = std::min(std::max((j - first) / (last - first), 0.0), 1.0);
+      f = f / factor * ramp + f * (1.0 - ramp);
+    } else if (scaling == PA_ROPE_BANDS) {
+      const double turns = original_len * f / kTwoPi;  // original_len / wavelength
+      const double keep = std::min(std::max((turns - low) / (high - low), 0.0), 1.0);
+      f = f / factor * (1.0 - keep) + f * keep;
+    }
+    table[j] = f / kTwoPi;
+  }
+  *amplitude = scaling == PA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return PA_OK;
+}
+
+pa_status pa_rope(void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                  const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                  const int32_t* positions, const double* table, int rot_dim, int interleaved,
+                  float amplitude, const void* q_weight, const void* k_weight, float eps, int T,
+                  int H, int Hkv, int D, pa_dtype dt, void* stream) {
+  pa::RopeParams prm = rope_params(q_out, q_out_stride, q, q_stride, k, k_stride, positions, table,
+                                   rot_dim, amplitude, q_weight, k_weight, eps, T, H, Hkv, D);
+  if (!rope_args_ok(prm, dt)) return PA_ERR_INVALID;
+  if (T == 0 || H + Hkv == 0) return PA_OK;
+  if (!rope_pointers_ok(prm) || (Hkv > 0 && !rows_ok(k_out, k_out_stride, Hkv, D)))
+    return PA_ERR_INVALID;
+  prm.k_out = k_out;
+  prm.k_out_stride = k_out_stride;
+  return pa::host::launch_rope(prm, dt, interleaved, 0, static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_rope_append(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         const int32_t* positions, const int64_t* slot_mapping, void* k_cache,
+                         void* v_cache, const double* table, int rot_dim, int interleaved,
+                         float amplitude, const void* q_weight, const void* k_weight, float eps,
+                         int T, int H, int Hkv, int D, int S, int NB, pa_dtype dt, void* stream) {
+  pa::RopeParams prm = rope_params(q_out, q_out_stride, q, q_stride, k, k_stride, positions, table,
+                                   rot_dim, amplitude, q_weight, k_weight, eps, T, H, Hkv, D);
+  return rope_append(prm, v, v_stride, slot_mapping, k_cache, v_cache, S, NB, dt, interleaved, 1,
+                     stream);
+}
+
+pa_status pa_rope_append_fp8(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const int32_t* positions, const int64_t* slot_mapping, void* k_cache,
+                             void* v_cache, float k_scale, float v_scale, const double* table,
+                             int rot_dim, int interleaved, float amplitude, const void* q_weight,
+                             const void* k_weight, float eps, int T, int H, int Hkv, int D, int S,
+                             int NB, pa_dtype dt, void* stream) {
+  if (D % 16 != 0) return PA_ERR_INVALID;  // as pa_kv_append_fp8: 16-byte cache rows
+  if (!(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
+    return PA_ERR_INVALID;
+  pa::RopeParams prm = rope_params(q_out, q_out_stride, q, q_stride, k, k_stride, positions, table,
+                                   rot_dim, amplitude, q_weight, k_weight, eps, T, H, Hkv, D);
+  prm.k_scale = k_scale;
+  prm.v_scale = v_scale;
+  return rope_append(prm, v, v_stride, slot_mapping, k_cache, v_cache, S, NB, dt, interleaved, 2,
+                     stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// pa_cross and pa_decode_shared
+// ---------------------------------------------------------------------------
+
+namespace {
+
+constexpr int kKeyTile = 128;  // keys per tile of the rows kernel
+
+struct RowsPlan {
+  bool split_keys;  // the CTA's two halves on one row tile
+  int P, parts;     // keys per partition (a multiple of kKeyTile), partitions
+};
+
+// How the rows kernel's work is laid out: `items` with up to max_rows query
+// tokens each, G heads per KV head, keys up to max_len. The choice minimises an
+// estimate of the time, in units of one key tile with both halves on one row
+// tile: waves of CTAs (one per SM) x (key tiles per CTA x the tile's time + a
+// CTA's start and end), plus, where the keys are split, the merge.
+RowsPlan plan_rows(int items, int max_rows, int G, int Hkv, int D, int max_len, int partition) {
+  const int64_t tiles = std::max<int64_t>(1, ceil_div(max_len, kKeyTile));
+  const int qpt = kKeyTile / G;
+  const int64_t sms = sm_count();
+  RowsPlan best{};
+  double best_cost = 0.0;
+  bool any = false;
+  for (int split = D == 256 ? 0 : 1; split >= 0; --split) {
+    const int row_tiles = (split || D == 256) ? 1 : 2;
+    if (row_tiles == 2 && max_rows <= qpt) continue;  // nothing for the second half
+    const double tile_cost = split ? 1.0 : 2.0;
+    const int64_t ctas = static_cast<int64_t>(std::max(items, 1)) * Hkv *
+                         std::max<int64_t>(1, ceil_div(max_rows, row_tiles * qpt));
+    const int64_t most =
+        partition == 0 ? std::min(tiles, std::max<int64_t>(8, 2 * sms / ctas + 1)) : 1;
+    for (int64_t c = 1; c <= most; ++c) {
+      int64_t per = ceil_div(tiles, c);
+      if (partition > 0) per = partition / kKeyTile;
+      const int64_t parts = ceil_div(tiles, per);
+      const int64_t waves = ceil_div(ctas * parts, sms);
+      double cost = static_cast<double>(waves) * (per * tile_cost + 2.0);
+      if (parts > 1)  // the merge: its launch, and its reads and writes of the results
+        cost += 1.5 + static_cast<double>(items) * max_rows * Hkv * G * parts * D * 8.0 / 9.0e6;
+      if (!any || cost < best_cost) {
+        any = true;
+        best_cost = cost;
+        best.split_keys = split != 0;
+        best.parts = static_cast<int>(parts);
+        best.P = static_cast<int>(per * kKeyTile);
+      }
+    }
+  }
+  return best;
+}
+
+// (P is then at most INT_MAX)
+bool rows_len_ok(int max_len) { return max_len >= 0 && max_len <= INT_MAX - (kKeyTile - 1); }
+
+bool rows_shape_ok(int H, int Hkv, int D) {
+  return H > 0 && Hkv > 0 && H % Hkv == 0 && H / Hkv <= 128 && (D == 64 || D == 128 || D == 256);
+}
+
+struct SharedPlan {
+  RowsPlan rows;
+  int shared_parts, tail_P, tail_parts;
+};
+
+SharedPlan plan_shared(int B, int NG, int H, int Hkv, int D, int S, int max_group,
+                       int max_shared_len, int max_tail_len) {
+  SharedPlan s{};
+  s.rows = plan_rows(NG, max_group, H / Hkv, Hkv, D, max_shared_len, 0);
+  s.shared_parts = max_shared_len > 0 ? s.rows.parts : 0;
+  int P = 0, NP = 1;
+  plan_grouped(B, H, Hkv, S, max_tail_len, 0, &P, &NP);
+  s.tail_parts = max_tail_len > 0 ? NP : 0;
+  s.tail_P = P > 0 ? P : static_cast<int>(ceil_div(std::max(max_tail_len, 1), S) * S);
+  return s;
+}
+
+bool shared_bounds_ok(int B, int NG, int H, int Hkv, int D, int S, int max_group,
+                      int max_shared_len, int max_tail_len) {
+  return B >= 0 && NG >= 0 && B <= 65535 && NG <= 65535 && H <= 65535 && rows_shape_ok(H, Hkv, D) &&
+         decode_shape_ok(D, S) && max_group >= 0 && rows_len_ok(max_shared_len) &&
+         max_tail_len >= 0 && max_tail_len <= INT_MAX - 4096;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pa_cross_workspace_bytes(int B, int T, int H, int Hkv, int D, int max_q_len, int max_kv_len,
+                                int partition) {
+  if (B <= 0 || T <= 0 || max_q_len <= 0 || !rows_len_ok(max_kv_len) || !rows_shape_ok(H, Hkv, D))
+    return 0;
+  if (partition < -1 || (partition > 0 && partition % kKeyTile != 0)) return 0;
+  const RowsPlan pl = plan_rows(B, std::min(max_q_len, T), H / Hkv, Hkv, D, max_kv_len, partition);
+  return workspace_for(T, H, D, pl.parts);
+}
+
+pa_status pa_cross(void* out, pa_dtype out_dt, const void* q, const void* k_cache,
+                   const void* v_cache, const int32_t* block_tables, int MB,
+                   const int32_t* kv_lens, const int32_t* q_start, float scale, int B, int H,
+                   int Hkv, int D, int S, int NB, pa_dtype dt, int T, int max_q_len,
+                   int max_kv_len, int partition, void* workspace, size_t ws_bytes, void* stream) {
+  if (B < 0 || T < 0 || max_q_len < 0 || MB < 0 || NB < 0 || !rows_shape_ok(H, Hkv, D))
+    return PA_ERR_INVALID;
+  if (!cache_dtype_ok(dt) || !out_dtype_ok(out_dt)) return PA_ERR_INVALID;
+  if (!(S == 8 || S == 16 || S == 32 || S == 64 || S == 128)) return PA_ERR_INVALID;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID;
+  if (partition < -1 || (partition > 0 && partition % kKeyTile != 0)) return PA_ERR_INVALID;
+  const int64_t L_max = static_cast<int64_t>(MB) * S;
+  if (L_max > INT_MAX || !rows_len_ok(max_kv_len) || max_kv_len > L_max) return PA_ERR_INVALID;
+  if (B == 0 || T == 0 || max_q_len == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !kv_lens || !q_start || MB == 0)
+    return PA_ERR_INVALID;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PA_ERR_INVALID;
+  if (B > 65535 || NB == 0 || static_cast<int64_t>(NB) * Hkv * S > INT_MAX) return PA_ERR_INVALID;
+  const int G = H / Hkv;
+  const int max_rows = std::min(max_q_len, T);
+  const RowsPlan pl = plan_rows(B, max_rows, G, Hkv, D, max_kv_len, partition);
+  // grid: x row tiles and KV heads (merge: row and head pairs), y partitions
+  if (static_cast<int64_t>(max_rows) * H > INT_MAX || pl.parts > 65535) return PA_ERR_INVALID;
+  const size_t need = workspace_for(T, H, D, pl.parts);
+  if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return PA_ERR_INVALID;
+  pa::RowsParams prm{};
+  prm.out = out;
+  prm.out_dt = out_dt;
+  prm.k_cache = k_cache;
+  prm.v_cache = v_cache;
+  prm.block_tables = block_tables;
+  prm.lens = kv_lens;
+  prm.start = q_start;
+  prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  prm.MB = MB;
+  prm.items = B;
+  prm.H = H;
+  prm.Hkv = Hkv;
+  prm.NB = NB;
+  prm.T = T;
+  prm.S = S;
+  prm.max_rows = max_rows;
+  prm.L_cap = max_kv_len;
+  prm.P = pl.P;
+  prm.parts = prm.NP = pl.parts;
+  prm.qpt = kKeyTile / G;
+  if (need > 0) {
+    const size_t n = static_cast<size_t>(T) * H * pl.parts;
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    prm.ws_m = reinterpret_cast<float*>(base);
+    prm.ws_l = prm.ws_m + n;
+    prm.ws_acc = reinterpret_cast<float*>(base + acc_offset(n));
+  }
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const pa_status rc = pa::host::launch_rows(prm, q, dt, D, pl.split_keys, st);
+  return rc != PA_OK ? rc : pa::host::launch_cross_merge(prm, D, st);
+}
+
+size_t pa_decode_shared_workspace_bytes(int B, int NG, int H, int Hkv, int D, int S, int max_group,
+                                        int max_shared_len, int max_tail_len) {
+  if (!shared_bounds_ok(B, NG, H, Hkv, D, S, max_group, max_shared_len, max_tail_len) || B == 0)
+    return 0;
+  const SharedPlan pl = plan_shared(B, NG, H, Hkv, D, S, std::min(max_group, B), max_shared_len,
+                                    max_tail_len);
+  const size_t n = static_cast<size_t>(B) * H * (pl.shared_parts + pl.tail_parts);
+  return n == 0 ? 0 : acc_offset(n) + n * D * sizeof(float);
+}
+
+pa_status pa_decode_shared(void* out, pa_dtype out_dt, const void* q, const void* k_cache,
+                           const void* v_cache, const int32_t* block_tables, int MB,
+                           const int32_t* seq_lens, const int32_t* shared_lens,
+                           const int32_t* group_start, int NG, float scale, int B, int H, int Hkv,
+                           int D, int S, int NB, pa_dtype dt, int max_group, int max_shared_len,
+                           int max_tail_len, void* workspace, size_t ws_bytes, void* stream) {
+  if (!shared_bounds_ok(B, NG, H, Hkv, D, S, max_group, max_shared_len, max_tail_len))
+    return PA_ERR_INVALID;
+  if (!cache_dtype_ok(dt) || !out_dtype_ok(out_dt) || MB < 0 || NB < 0) return PA_ERR_INVALID;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID;
+  const int64_t L_max = static_cast<int64_t>(MB) * S;
+  if (L_max > INT_MAX || max_shared_len > L_max || max_tail_len > L_max) return PA_ERR_INVALID;
+  if (B == 0) return PA_OK;
+  // every request belongs to a group
+  if (NG == 0 || max_group == 0) return PA_ERR_INVALID;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !shared_lens ||
+      !group_start || MB == 0)
+    return PA_ERR_INVALID;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PA_ERR_INVALID;
+  if (NB == 0 || static_cast<int64_t>(NB) * Hkv * S > INT_MAX) return PA_ERR_INVALID;
+  const int G = H / Hkv;
+  max_group = std::min(max_group, B);
+  const SharedPlan pl = plan_shared(B, NG, H, Hkv, D, S, max_group, max_shared_len, max_tail_len);
+  const int NP = pl.shared_parts + pl.tail_parts;
+  const size_t n = static_cast<size_t>(B) * H * NP;
+  const size_t need = n == 0 ? 0 : acc_offset(n) + n * D * sizeof(float);
+  if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return PA_ERR_INVALID;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  float* ws_m = reinterpret_cast<float*>(base);
+  float* ws_l = need > 0 ? ws_m + n : nullptr;
+  float* ws_acc = need > 0 ? reinterpret_cast<float*>(base + acc_offset(n)) : nullptr;
+  const double scale_log2 = static_cast<double>(scale) * 1.4426950408889634;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  if (pl.shared_parts > 0) {
+    pa::RowsParams prm{};
+    prm.k_cache = k_cache;
+    prm.v_cache = v_cache;
+    prm.block_tables = block_tables;
+    prm.lens = seq_lens;
+    prm.shared_lens = shared_lens;
+    prm.start = group_start;
+    prm.ws_m = ws_m;
+    prm.ws_l = ws_l;
+    prm.ws_acc = ws_acc;
+    prm.scale_log2 = static_cast<float>(scale_log2);
+    prm.MB = MB;
+    prm.items = NG;
+    prm.H = H;
+    prm.Hkv = Hkv;
+    prm.NB = NB;
+    prm.T = B;
+    prm.S = S;
+    prm.max_rows = max_group;
+    prm.L_cap = max_shared_len;
+    prm.P = pl.rows.P;
+    prm.parts = pl.rows.parts;
+    prm.NP = NP;
+    prm.qpt = kKeyTile / G;
+    const pa_status rc = pa::host::launch_rows(prm, q, dt, D, pl.rows.split_keys, st);
+    if (rc != PA_OK) return rc;
+  }
+  pa::DecodeParamsTail t{};
+  t.out = out;
+  t.q = q;
+  t.k_cache = k_cache;
+  t.v_cache = v_cache;
+  t.block_tables = block_tables;
+  t.seq_lens = seq_lens;
+  t.shared_lens = shared_lens;
+  t.ws_m = ws_m;
+  t.ws_l = ws_l;
+  t.ws_acc = ws_acc;
+  t.q_scale = static_cast<float>(scale_log2);
+  t.v_scale = 1.f;
+  t.MB = MB;
+  t.B = B;
+  t.H = H;
+  t.Hkv = Hkv;
+  t.NB = NB;
+  t.P = pl.tail_P;
+  t.NP = NP;
+  t.L_cap = max_tail_len;
+  t.part0 = pl.shared_parts;
+  t.shared_cap = max_shared_len;
+  t.tail_parts = pl.tail_parts;
+  if (pl.tail_parts > 0) {
+    const pa_status rc = pa::host::launch_tails(t, dt, D, S, st);
+    if (rc != PA_OK) return rc;
+  }
+  return pa::host::launch_shared_merge(t, pl.rows.P, out_dt, D, S, st);
+}
+
+}  // extern "C"

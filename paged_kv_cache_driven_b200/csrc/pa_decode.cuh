@@ -140,6 +140,13 @@ __device__ __forceinline__ void quantize_e4m3(const uint32_t (&x)[EL / 2], float
   }
 }
 
+// The tokens of a request that a batch with shared prefixes reads for its whole
+// group: whole blocks inside both its shared length and its length.
+__device__ __forceinline__ int shared_part(int shared, int len, int cap, int S) {
+  const int s = max(0, min(min(shared, len), cap));
+  return s - s % S;
+}
+
 // One CTA per (partition, head, request); NW warps, each an independent
 // pipeline over the tokens of a contiguous run of the partition's blocks,
 // taken CR rows (one unit) at a time.
@@ -197,13 +204,25 @@ __global__ void __launch_bounds__(DecodeTiling<D, S, sizeof(TC), WIDE>::NW * 32)
   const int pl = lane % LPR;  // position in the row: elements pl * EPL .. pl * EPL + EPL - 1
 
   int L = __ldg(p.seq_lens + i);
+  // The tails of a batch with shared prefixes (DecodeParamsTail): the tokens
+  // behind the first `skip`; every partition leaves its result in the workspace.
+  constexpr bool TAIL = std::is_same<Prm, DecodeParamsTail>::value;
+  int skip = 0;
+  if constexpr (TAIL) {
+    if (L > p.MB * S) {  // past the table's row
+      if (threadIdx.x == 0 && part == 0 && h == 0) raise_error(PA_DEVERR_SEQ_LEN);
+      L = p.MB * S;
+    }
+    skip = shared_part(__ldg(p.shared_lens + i), L, p.shared_cap, S);
+    L -= skip;
+  }
   const bool len_ok = L >= 0 && L <= p.L_cap;
   if (!len_ok) {
     if (threadIdx.x == 0 && part == 0 && h == 0) raise_error(PA_DEVERR_SEQ_LEN);
     L = L < 0 ? 0 : p.L_cap;
   }
   const int nparts = (L + p.P - 1) / p.P;
-  if (part > 0 && part >= nparts) {  // nothing here (part 0 writes the L == 0 zeros)
+  if ((TAIL || part > 0) && part >= nparts) {  // nothing here (part 0 writes the L == 0 zeros)
     if constexpr (clustered) {
       cluster_wait_acquire();
       cluster_arrive_release();
@@ -211,7 +230,7 @@ __global__ void __launch_bounds__(DecodeTiling<D, S, sizeof(TC), WIDE>::NW * 32)
     }
     return;
   }
-  const bool direct = nparts <= 1;  // the only partition: write the final output
+  const bool direct = !TAIL && nparts <= 1;  // the only partition: write the final output
 
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Tl::SMEM_PIPE);
@@ -274,7 +293,7 @@ __global__ void __launch_bounds__(DecodeTiling<D, S, sizeof(TC), WIDE>::NW * 32)
 
   uint64_t* bar = bars + w * NS;
   uint8_t* stage0 = smem + w * NS * STAGE;
-  const int32_t* trow = p.block_tables + static_cast<int64_t>(i) * p.MB;
+  const int32_t* trow = p.block_tables + static_cast<int64_t>(i) * p.MB + skip / S;
   const int hk = h / (p.H / p.Hkv);  // this query head's KV head
   const uint8_t* kbase = static_cast<const uint8_t*>(p.k_cache) + static_cast<int64_t>(hk) * SLAB;
   const uint8_t* vbase = static_cast<const uint8_t*>(p.v_cache) + static_cast<int64_t>(hk) * SLAB;
@@ -535,6 +554,8 @@ __global__ void __launch_bounds__(DecodeTiling<D, S, sizeof(TC), WIDE>::NW * 32)
     Ltot = fmaf(wgt[u], l_s[u], Ltot);
   }
   const int64_t ih = static_cast<int64_t>(i) * p.H + h;
+  int64_t wslot = ih * p.NP + part;  // this result's place in the workspace
+  if constexpr (TAIL) wslot += p.part0;
   // Cluster launch: this partition's (acc, m, l) go to its slot in partition
   // 0's shared memory (every CTA of the cluster has started once the first
   // barrier is passed).
@@ -555,7 +576,7 @@ __global__ void __launch_bounds__(DecodeTiling<D, S, sizeof(TC), WIDE>::NW * 32)
     } else if constexpr (clustered) {
       st_cluster_f32(xrem + d * 4, a);
     } else {
-      p.ws_acc[(ih * p.NP + part) * D + d] = a;
+      p.ws_acc[wslot * D + d] = a;
     }
   }
   if (!direct && threadIdx.x == 0) {
@@ -563,8 +584,8 @@ __global__ void __launch_bounds__(DecodeTiling<D, S, sizeof(TC), WIDE>::NW * 32)
       st_cluster_f32(xrem + D * 4, M);
       st_cluster_f32(xrem + (D + 1) * 4, Ltot);
     } else {
-      p.ws_m[ih * p.NP + part] = M;
-      p.ws_l[ih * p.NP + part] = Ltot;
+      p.ws_m[wslot] = M;
+      p.ws_l[wslot] = Ltot;
     }
   }
   if constexpr (clustered) {

@@ -136,9 +136,13 @@ __device__ __forceinline__ float2 unpack2(uint32_t x) {
 // into q_scale, V's applied to the output). Over E4M3 the consumers convert
 // each staged unit to f16 tiles and the products run in f16 (E4M3 values are
 // f16 values), with q held in f16 after an exact power-of-two scaling per head.
-template <typename T, typename TO, int D, int S, bool APPEND, int NHT, typename TC = T>
+// Prm = DecodeParamsTail: the tails of a batch with shared prefixes, the tokens
+// behind each request's shared part; every partition leaves its result in the
+// workspace.
+template <typename T, typename TO, int D, int S, bool APPEND, int NHT, typename TC = T,
+          typename Prm = DecodeParams>
 __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
-    paged_decode_gqa_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
+    paged_decode_gqa_kernel(const Prm p, const __grid_constant__ CUtensorMap tmk,
                             const __grid_constant__ CUtensorMap tmv) {
   constexpr int EB = sizeof(TC);
   static_assert(!APPEND || EB == 2, "no fused append over E4M3 caches here");
@@ -167,22 +171,34 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
   const int t_beg = part * p.P;
   const int blk0 = t_beg / S;
   const int32_t* trow = p.block_tables + static_cast<int64_t>(i) * p.MB;
+  int width = p.MB;  // entries of the table row from trow on
+  constexpr bool TAIL = std::is_same<Prm, DecodeParamsTail>::value;
+  int L = __ldg(p.seq_lens + i);
+  if constexpr (TAIL) {
+    if (L > p.MB * S) {  // past the table's row
+      if (threadIdx.x == 0 && part == 0 && blockIdx.y == 0) raise_error(PA_DEVERR_SEQ_LEN);
+      L = p.MB * S;
+    }
+    const int skip = shared_part(__ldg(p.shared_lens + i), L, p.shared_cap, S);
+    L -= skip;
+    trow += skip / S;
+    width -= skip / S;
+  }
   int ids_a = -1, ids_b = -1;
   auto load_ids = [&](int blk1) {
-    const int lim = min(blk1, p.MB);
+    const int lim = min(blk1, width);
     ids_a = (blk0 + lane < lim) ? __ldg(trow + blk0 + lane) : -1;
     ids_b = (blk0 + 32 + lane < lim) ? __ldg(trow + blk0 + 32 + lane) : -1;
   };
   if (w == NC) load_ids(blk0 + p.P / S);
-  int L = __ldg(p.seq_lens + i);
   const bool len_ok = L >= 0 && L <= p.L_cap;
   if (!len_ok) {
     if (threadIdx.x == 0 && part == 0 && blockIdx.y == 0) raise_error(PA_DEVERR_SEQ_LEN);
     L = L < 0 ? 0 : p.L_cap;
   }
   const int nparts = (L + p.P - 1) / p.P;
-  if (part > 0 && part >= nparts) return;
-  const bool direct = nparts <= 1;
+  if ((TAIL || part > 0) && part >= nparts) return;
+  const bool direct = !TAIL && nparts <= 1;
 
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -652,6 +668,8 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
     }
     const int64_t hq = static_cast<int64_t>(hk) * G + c0 + row;
     const int64_t ih = static_cast<int64_t>(i) * p.H + hq;
+    int64_t wslot = ih * p.NP + part;  // this result's place in the workspace
+    if constexpr (TAIL) wslot += p.part0;
     for (int d = lane; d < D; d += 32) {
       float a = 0.f;
 #pragma unroll
@@ -660,12 +678,12 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
       if (direct) {
         static_cast<TO*>(p.out)[ih * D + d] = to_out<TO>(lsum > 0.f ? a / lsum : 0.f);
       } else {
-        p.ws_acc[(ih * p.NP + part) * D + d] = a;
+        p.ws_acc[wslot * D + d] = a;
       }
     }
     if (!direct && lane == 0) {
-      p.ws_m[ih * p.NP + part] = M;
-      p.ws_l[ih * p.NP + part] = lsum;
+      p.ws_m[wslot] = M;
+      p.ws_l[wslot] = lsum;
     }
   }
 }

@@ -1,0 +1,65 @@
+// Kernels of pa_rope, pa_rope_append and pa_rope_append_fp8, for both 16-bit
+// types, both pair layouts and every head size, and their launcher.
+
+#include <algorithm>
+
+#include "pa_launch.h"
+#include "pa_rope.cuh"
+
+namespace pa {
+namespace host {
+namespace {
+
+template <typename T, int LAYOUT, int MODE, int LPR>
+pa_status launch(RopeParams prm, cudaStream_t stream) {
+  // One CTA per token where the tokens fill the GPU. Fewer tokens have their
+  // rows spread over up to two CTAs per SM, down to one row per thread.
+  constexpr int RPP = 256 / LPR;
+  const int64_t most = ceil_div(prm.rows, RPP);
+  const int64_t want = ceil_div(2 * static_cast<int64_t>(sm_count()), prm.T);
+  int64_t chunks = std::max<int64_t>(1, std::min(most, want));
+  prm.chunk_rows = static_cast<int>(ceil_div(ceil_div(prm.rows, chunks), RPP) * RPP);
+  chunks = ceil_div(prm.rows, prm.chunk_rows);
+  prm.chunks = static_cast<int>(chunks);
+  // (chunks > 1 only where T is at most 2 CTAs per SM: the product stays small)
+  rope_kernel<T, LAYOUT, MODE, LPR>
+      <<<static_cast<unsigned>(prm.T * chunks), 256, 0, stream>>>(prm);
+  return cuda_status();
+}
+
+template <typename T, int LAYOUT, int MODE>
+pa_status by_size(const RopeParams& prm, cudaStream_t st) {
+  if (prm.D <= 64) return launch<T, LAYOUT, MODE, 8>(prm, st);
+  if (prm.D <= 128) return launch<T, LAYOUT, MODE, 16>(prm, st);
+  return launch<T, LAYOUT, MODE, 32>(prm, st);
+}
+
+template <typename T, int MODE>
+pa_status by_layout(const RopeParams& prm, int interleaved, cudaStream_t st) {
+  if (interleaved) return by_size<T, kPairs, MODE>(prm, st);
+  return prm.rot % 8 == 0 ? by_size<T, kHalf, MODE>(prm, st)
+                          : by_size<T, kHalfAny, MODE>(prm, st);
+}
+
+template <typename T>
+pa_status by_mode(const RopeParams& prm, int interleaved, int mode, cudaStream_t st) {
+  switch (mode) {
+    case kNoCache: return by_layout<T, kNoCache>(prm, interleaved, st);
+    case kCache16: return by_layout<T, kCache16>(prm, interleaved, st);
+    case kCache8: return by_layout<T, kCache8>(prm, interleaved, st);
+  }
+  return PA_ERR_INVALID;
+}
+
+}  // namespace
+
+pa_status launch_rope(const RopeParams& prm, pa_dtype dt, int interleaved, int mode,
+                      cudaStream_t stream) {
+  return dt == PA_BF16 ? by_mode<__nv_bfloat16>(prm, interleaved, mode, stream)
+                       : by_mode<__half>(prm, interleaved, mode, stream);
+}
+
+bool take_error_rope(unsigned int* bits) { return take_error_word(bits); }
+
+}  // namespace host
+}  // namespace pa

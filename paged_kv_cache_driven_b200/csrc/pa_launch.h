@@ -55,6 +55,64 @@ struct PrefillParams {
   int MB, B, H, Hkv, NB, T, max_q_len;
 };
 
+// pa_rope / pa_rope_append / pa_rope_append_fp8. Strides in elements per token.
+struct RopeParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_out;                // pa_rope
+  void* k_cache;              // the append forms: [NB, Hkv, S, D]
+  void* v_cache;
+  const int32_t* positions;   // [T]
+  const int64_t* slots;       // [T], the append forms
+  const double* table;        // [rot / 2] turns per position
+  const void* q_weight;       // [D] or null
+  const void* k_weight;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  int64_t n_slots;            // NB * S
+  float eps, amplitude, k_scale, v_scale;
+  int T, H, Hkv, D, rot, S;
+  int rows;                   // rows per token: H + Hkv, + Hkv with the append
+  int chunks;                 // CTAs per token
+  int chunk_rows;             // rows per CTA
+};
+
+// Attention of packed query rows over whole paged key ranges (pa_cross, and the
+// shared part of pa_decode_shared): item i (a request, or a group of requests)
+// has the query rows start[i] .. start[i + 1] - 1.
+struct RowsParams {
+  void* out;                    // [T, H, D] out_dt
+  const void* k_cache;          // [NB, Hkv, S, D]
+  const void* v_cache;
+  const int32_t* block_tables;  // [., MB]: row i, or (shared) row of a request
+  const int32_t* lens;          // pa_cross: [items] keys; shared: [T] seq_lens
+  const int32_t* shared_lens;   // null for pa_cross; shared: [T]
+  const int32_t* start;         // [items + 1]
+  float* ws_m;                  // [T, H, NP]
+  float* ws_l;
+  float* ws_acc;                // [T, H, NP, D]
+  float scale_log2;             // scale * log2(e)
+  int MB, items, H, Hkv, NB, T, S;
+  int max_rows;                 // host bound on an item's query rows
+  int L_cap;                    // lengths are clamped to this
+  int P;                        // keys per partition, a multiple of 128
+  int parts;                    // partitions in the grid
+  int NP;                       // result slots per (row, head) in the workspace
+  int qpt;                      // query rows (tokens) per 128-row tile: 128 / (H / Hkv)
+  pa_dtype out_dt;
+};
+
+// The tails of pa_decode_shared: the decode kernels' partition pass over the
+// tokens behind each request's shared part, every partition's result going to
+// slot part0 + partition of the workspace's NP slots.
+struct DecodeParamsTail : DecodeParams {
+  const int32_t* shared_lens;  // [B]
+  int part0;
+  int shared_cap;              // host bound on shared_lens
+  int tail_parts;              // partitions in the grid
+};
+
 namespace host {
 
 constexpr int kMaxDevices = 64;
@@ -82,10 +140,21 @@ bool opt_in_smem(K kern, int bytes, bool (&configured)[kMaxDevices]) {
 // box_rows rows, 128-byte swizzle (the last few maps are cached). query_map: the
 // packed queries [T, H, D] as (D, H, T), boxes of 64 elements x 1 head x 128 rows.
 bool row_map(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows, pa_dtype dt);
+// row_map_now: the same, encoded anew at each call.
+bool row_map_now(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows,
+                 pa_dtype dt);
 // row_map_codes: the same view of a cache of one-byte E4M3 codes; a box is one
 // whole D-byte row x box_rows rows, unswizzled.
 bool row_map_codes(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows);
 bool query_map(CUtensorMap* out, const void* q, int64_t T, int H, int D, pa_dtype dt);
+
+// query_rows_map: the same view of the queries, boxes of 64 elements x `heads`
+// heads x `rows` rows (heads * rows <= 128).
+bool query_rows_map(CUtensorMap* out, const void* q, int64_t T, int H, int D, int heads, int rows,
+                    pa_dtype dt);
+
+// SMs of the current device (148 on B200; also the answer without a device).
+int sm_count();
 
 // Launchers (asynchronous on `stream`; the arguments are already checked).
 // cluster: launch the partition pass in clusters of prm.NP CTAs (NP of 2, 4
@@ -118,12 +187,28 @@ pa_status launch_kv_append_fp8(const void* k, const void* v, pa_dtype in_dt,
 pa_status launch_copy_blocks(void* k_cache, void* v_cache, const int32_t* src_dst, int n, int H,
                              int S, int D, int NB, cudaStream_t stream);
 
+// mode: 0 = keys to k_out, 1 = keys and values to 16-bit caches, 2 = to E4M3 caches
+pa_status launch_rope(const RopeParams& prm, pa_dtype dt, int interleaved, int mode,
+                      cudaStream_t stream);                             // pa_k_rope.cu
+// split_keys: the CTA's two halves take alternate key tiles of one row tile
+// (items of at most one row tile), else the same key tiles of two row tiles
+pa_status launch_rows(const RowsParams& prm, const void* q, pa_dtype dt, int D, bool split_keys,
+                      cudaStream_t stream);                             // pa_k_rows.cu
+pa_status launch_cross_merge(const RowsParams& prm, int D, cudaStream_t stream);
+pa_status launch_tails(const DecodeParamsTail& prm, pa_dtype dt, int D, int S,
+                       cudaStream_t stream);                            // pa_k_shared.cu
+pa_status launch_shared_merge(const DecodeParamsTail& prm, int P_shared, pa_dtype out_dt, int D,
+                              int S, cudaStream_t stream);
+
 // Each unit's device error word, read and cleared (ORed into *bits).
 bool take_error_decode16(unsigned int* bits);
 bool take_error_grouped(unsigned int* bits);
 bool take_error_fp8(unsigned int* bits);
 bool take_error_prefill(unsigned int* bits);
 bool take_error_append(unsigned int* bits);
+bool take_error_rope(unsigned int* bits);
+bool take_error_rows(unsigned int* bits);
+bool take_error_shared(unsigned int* bits);
 
 }  // namespace host
 }  // namespace pa

@@ -1,0 +1,697 @@
+// Attention of packed query rows over whole paged key ranges, on the
+// fifth-generation tensor cores: pa_cross, and the shared part of
+// pa_decode_shared.
+//
+// What it computes: item i (a request's queries, or the queries of a group of
+// requests) has the query tokens start[i] .. start[i+1] - 1, and every one of
+// them sees the same keys, tokens 0 .. L - 1 of one block table:
+//   out[r, h] = softmax_t(scale * q[r, h] . K_t) V_t,   no causal mask.
+// The G = H / Hkv query heads of a KV head read the same keys too, so the rows
+// of one contraction are (token, head of the group) pairs: a 128-row tile is
+// qpt = 128 / G tokens x G heads, loaded by one TMA box per 64-element column
+// block (box 64 x G heads x qpt tokens), row r = token r / G, head r % G. K and V
+// are thus read once for all of a tile's tokens and heads.
+//
+// One CTA per (row tiles, KV head, partition of the keys, item), 576 threads (320
+// at head size 256) in the roles of the causal prefill kernel: two softmax
+// warpgroups per stream, a producer warp (one lane per cache block and TMA box),
+// an MMA issuer warp that also owns tensor memory. Two streams ping-pong, so
+// that the tensor cores work for one while the other's softmax runs:
+//   KSPLIT = false  stream t takes row tile t: both read every key tile;
+//   KSPLIT = true   one row tile (few rows): stream t takes the key tiles
+//                   t, t + 2, ..., and the CTA joins the two results at its end
+//                   through the K ring's memory. A key tile then costs half the
+//                   time, which brings few rows over long keys close to the
+//                   rate at which HBM delivers the keys.
+// Few CTAs are multiplied by partitions of the keys, whose results (m, l, O) a
+// merge kernel joins. Scores, softmax statistics and output accumulate in fp32;
+// the weights enter the second product as two bf16 terms (value and rounding
+// residue) for bf16, as one f16 term for f16.
+//
+// Every wait is bounded (about a second); a timeout sets PA_DEVERR_TIMEOUT, stops
+// all roles, waits for the copies and MMAs in flight and frees tensor memory.
+#pragma once
+
+#include <cuda.h>
+
+#include "pa_decode.cuh"
+#include "pa_prefill.cuh"
+
+namespace pa {
+
+template <int D, bool KSPLIT>
+struct RowsTiling {
+  static constexpr int BM = 128;              // query rows per tile (MMA M)
+  static constexpr int BN = 128;              // keys per tile
+  // streams: two, or one at head size 256 (tensor memory and shared memory, as
+  // in the prefill kernel)
+  static constexpr int NST = D == 256 ? 1 : 2;
+  static constexpr int NQ = KSPLIT ? 1 : NST;  // query tiles held
+  static constexpr int KST = D == 256 ? 1 : (D == 128 ? 2 : 4);  // K stages
+  static constexpr int VST = KST;                                // V stages
+  static constexpr int LEAD = KSPLIT ? 2 : 1;  // key tiles K runs ahead of V
+  static constexpr int COLB = D / 64;
+  static constexpr int CB_BYTES = 128 * 128;  // one column block of 128 rows
+  static constexpr int Q_BYTES = BM * D * 2;
+  static constexpr int KV_BYTES = BN * D * 2;
+  static constexpr int OFF_K = NQ * Q_BYTES;
+  static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
+  static constexpr int OFF_XCH = OFF_V + VST * KV_BYTES;
+  static constexpr int XCH_BYTES = NST * 2 * 2 * BM * 4;  // [stream][phase parity][half][row]
+  static constexpr int OFF_BAR = OFF_XCH + XCH_BYTES;
+  // at least 120 KB, so that one CTA holds an SM (it allocates all 512
+  // tensor-memory columns)
+  static constexpr int SMEM = 1024 + OFF_BAR + 256 > 120 * 1024 ? 1024 + OFF_BAR + 256 : 120 * 1024;
+  static constexpr int THREADS = NST * 256 + 64;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static_assert(!KSPLIT || NST == 2, "two streams share the keys");
+  static_assert(KST >= LEAD || D == 256, "K runs LEAD tiles ahead");
+  static_assert(!KSPLIT || D * 128 * 4 <= KST * KV_BYTES, "the join's O fits the K ring");
+  static_assert(SMEM <= 232448, "shared memory per CTA");
+};
+
+// 32 consecutive output elements of one row.
+__device__ __forceinline__ void store_out32(void* out, pa_dtype dt, int64_t at,
+                                            const float (&v)[32]) {
+  if (dt == PA_F32)
+    store_row32<float>(static_cast<float*>(out) + at, v);
+  else if (dt == PA_BF16)
+    store_row32<__nv_bfloat16>(static_cast<__nv_bfloat16*>(out) + at, v);
+  else
+    store_row32<__half>(static_cast<__half*>(out) + at, v);
+}
+
+template <typename T, int D, bool KSPLIT>
+__global__ void __launch_bounds__(576, 1)
+    rows_kernel(const RowsParams p, const __grid_constant__ CUtensorMap tmq,
+                const __grid_constant__ CUtensorMap tmk,
+                const __grid_constant__ CUtensorMap tmv) {
+  constexpr bool LO = std::is_same<T, __nv_bfloat16>::value;
+  using Tl = RowsTiling<D, KSPLIT>;
+  constexpr int NST = Tl::NST, BN = Tl::BN;
+
+  grid_dependents_launch();  // what follows on the stream may be scheduled early
+  const int G = p.H / p.Hkv;
+  const int qpt = p.qpt;
+  const int tok_cta = Tl::NQ * qpt;  // query tokens per CTA
+  const int ngroups = (p.max_rows + tok_cta - 1) / tok_cta;
+  const int hk = blockIdx.x / ngroups;
+  const int tok0 = (blockIdx.x - hk * ngroups) * tok_cta;
+  const int part = blockIdx.y, i = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.S;
+
+  const int q0 = p.start[i], q1 = p.start[i + 1];
+  const int n = q1 - q0;
+  const bool first_cta = blockIdx.x == 0 && part == 0;
+  if (n < 0 || q0 < 0 || q1 > p.T || n > p.max_rows) {
+    if (threadIdx.x == 0 && first_cta) raise_error(PA_DEVERR_SEQ_LEN);
+    return;
+  }
+  if (tok0 >= n) return;
+  const int ntok = min(n - tok0, tok_cta);
+  // the keys, and the row of the block table that names them
+  int L, trow = i;
+  if (p.shared_lens) {
+    // the longest shared part of the CTA's requests, through that request's table
+    int best = 0, who = q0 + tok0;
+    for (int r = lane; r < ntok; r += 32) {
+      const int b = q0 + tok0 + r;
+      const int sh = p.shared_lens[b], len = p.lens[b];
+      if (warp == 0 && hk == 0 && part == 0 && (sh < 0 || sh > p.L_cap || len < 0))
+        raise_error(PA_DEVERR_SEQ_LEN);
+      const int e = shared_part(sh, len, p.L_cap, S);
+      if (e > best) best = e, who = b;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      const int e = __shfl_xor_sync(kFullMask, best, o), b = __shfl_xor_sync(kFullMask, who, o);
+      if (e > best || (e == best && b < who)) best = e, who = b;
+    }
+    L = best;
+    trow = who;
+  } else {
+    L = p.lens[i];
+    if (L < 0 || L > p.L_cap) {
+      if (threadIdx.x == 0 && first_cta) raise_error(PA_DEVERR_SEQ_LEN);
+      L = L < 0 ? 0 : p.L_cap;
+    }
+  }
+  const int64_t t_beg64 = static_cast<int64_t>(part) * p.P;
+  const bool direct = !p.shared_lens && L <= p.P;  // the only partition: final output
+  if (t_beg64 >= L) {
+    if (direct && part == 0)  // no keys at all: zero rows
+      for (int64_t e = threadIdx.x; e < static_cast<int64_t>(ntok) * G * D; e += blockDim.x) {
+        const int64_t row = e / (G * D);
+        const int64_t at = (static_cast<int64_t>(q0 + tok0 + row) * p.H + hk * G) * D +
+                           (e - row * (G * D));
+        if (p.out_dt == PA_F32)
+          static_cast<float*>(p.out)[at] = 0.f;
+        else
+          static_cast<uint16_t*>(p.out)[at] = 0;
+      }
+    return;
+  }
+  const int t_beg = static_cast<int>(t_beg64);
+  const int t_end = static_cast<int>(min(t_beg64 + p.P, static_cast<int64_t>(L)));
+  const int NK = (t_end - t_beg + BN - 1) / BN;  // key tiles of the CTA
+  // key tiles each stream takes, and its query tokens' rows
+  int nk[NST], nrow[NST];
+#pragma unroll
+  for (int t = 0; t < NST; ++t) {
+    if constexpr (KSPLIT) {
+      nk[t] = (NK + 1 - t) >> 1;
+      nrow[t] = ntok * G;
+    } else {
+      nrow[t] = max(0, min(qpt, ntok - t * qpt)) * G;
+      nk[t] = nrow[t] > 0 ? NK : 0;
+    }
+  }
+  const int nq = KSPLIT ? 1 : (nrow[NST - 1] > 0 ? NST : 1);  // query tiles holding rows
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = sm;
+  uint8_t* sK = sm + Tl::OFF_K;
+  uint8_t* sV = sm + Tl::OFF_V;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Tl::OFF_BAR);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;             // [KST]
+  uint64_t* k_empty = k_full + Tl::KST;    // [KST]
+  uint64_t* v_full = k_empty + Tl::KST;    // [VST]
+  uint64_t* v_empty = v_full + Tl::VST;    // [VST]
+  uint64_t* s_full = v_empty + Tl::VST;    // [NST]
+  uint64_t* p_full = s_full + NST;         // [NST]
+  uint64_t* o_done = p_full + NST;         // [NST]
+  uint64_t* xch_bar = o_done + NST;        // [NST]: the stream's two halves have posted
+  uint64_t* mma_done = xch_bar + NST;
+  float* xch = reinterpret_cast<float*>(sm + Tl::OFF_XCH);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((1 + 2 * Tl::KST + 2 * Tl::VST + 4 * NST + 1) * 8 + 8 <= 256, "barriers");
+
+  constexpr int kProducer = 8 * NST, kIssuer = kProducer + 1;
+  const int bpt = BN / S;  // cache blocks per key tile
+  const int blk0 = t_beg / S, nblk = (t_end + S - 1) / S;
+  const int32_t* table = p.block_tables + static_cast<int64_t>(trow) * p.MB;
+  // this lane's block id in key tile j (-1: none or invalid)
+  auto block_id = [&](int j) {
+    const int lb = blk0 + j * bpt + lane;
+    int id = -1;
+    if (lane < bpt && lb < nblk) {
+      id = table[lb];
+      if (id < 0 || id >= p.NB) {
+        raise_error(PA_DEVERR_BLOCK_ID);
+        id = -1;
+      }
+    }
+    return id;
+  };
+  // one K or V tile: every lane issues the boxes of its block
+  auto load_tile = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full, int id) {
+    const int nvalid = __popc(__ballot_sync(kFullMask, id >= 0));
+    if (lane == 0)
+      mbar_arrive_expect_tx(full, static_cast<uint32_t>(nvalid) * S * 128 * Tl::COLB);
+    __syncwarp();
+    if (id >= 0) {
+      const int y = (id * p.Hkv + hk) * S;
+#pragma unroll
+      for (int c = 0; c < Tl::COLB; ++c)
+        tma_load_2d_nohint(dst + c * Tl::CB_BYTES + lane * S * 128, map, c * 64, y, full);
+    }
+  };
+  // The producer initialises the barriers and issues Q and the first K tiles
+  // before the CTA-wide sync, under the tensor-memory allocation.
+  int ids[Tl::LEAD + 1];  // block ids of key tiles j .. j + LEAD
+  if (warp == kProducer) {
+    if (lane == 0) {
+      mbar_init(q_full, 1);
+      for (int s = 0; s < Tl::KST; ++s) {
+        mbar_init(&k_full[s], 1);
+        mbar_init(&k_empty[s], 1);
+      }
+      for (int s = 0; s < Tl::VST; ++s) {
+        mbar_init(&v_full[s], 1);
+        mbar_init(&v_empty[s], 1);
+      }
+      for (int t = 0; t < NST; ++t) {
+        mbar_init(&s_full[t], 1);
+        mbar_init(&p_full[t], 256);
+        mbar_init(&o_done[t], 1);
+        mbar_init(&xch_bar[t], 256);
+      }
+      mbar_init(mma_done, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+#pragma unroll
+    for (int a = 0; a <= Tl::LEAD; ++a) ids[a] = a < NK ? block_id(a) : -1;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nq) * Tl::COLB * G * qpt * 128);
+      for (int t = 0; t < nq; ++t)
+#pragma unroll
+        for (int c = 0; c < Tl::COLB; ++c)
+          tc::tma_load_3d(sQ + t * Tl::Q_BYTES + c * Tl::CB_BYTES, &tmq, c * 64, hk * G,
+                          q0 + tok0 + t * qpt, q_full);
+    }
+#pragma unroll
+    for (int a = 0; a < Tl::LEAD; ++a)
+      if (a < NK) load_tile(&tmk, sK + (a % Tl::KST) * Tl::KV_BYTES, &k_full[a % Tl::KST], ids[a]);
+  }
+  if (warp == kIssuer) {
+    __syncwarp();
+    tc::tmem_alloc(tmem_slot, Tl::TMEM_COLS);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  if (warp == kProducer) {
+    // ---------------- producer ----------------
+    int k_issued = min(NK, Tl::LEAD), v_issued = 0;
+    auto next_k = [&](int j) {  // K(j + LEAD)
+      const int kj = j + Tl::LEAD, st = kj % Tl::KST;
+      if (kj >= NK) return true;
+      if (kj >= Tl::KST && !wait_warp(&k_empty[st], ((kj / Tl::KST) - 1) & 1, abort_flag))
+        return false;
+      load_tile(&tmk, sK + st * Tl::KV_BYTES, &k_full[st], ids[Tl::LEAD]);
+      k_issued = kj + 1;
+      return true;
+    };
+    auto next_v = [&](int j) {
+      const int st = j % Tl::VST;
+      if (j >= Tl::VST && !wait_warp(&v_empty[st], ((j / Tl::VST) - 1) & 1, abort_flag))
+        return false;
+      load_tile(&tmv, sV + st * Tl::KV_BYTES, &v_full[st], ids[0]);
+      v_issued = j + 1;
+      return true;
+    };
+    for (int j = 0; j < NK; ++j) {
+      // in the order in which their stages come free
+      if constexpr (KSPLIT) {
+        if (!next_v(j) || !next_k(j)) break;
+      } else {
+        if (!next_k(j) || !next_v(j)) break;
+      }
+#pragma unroll
+      for (int a = 0; a < Tl::LEAD; ++a) ids[a] = ids[a + 1];
+      if (j + Tl::LEAD + 1 < NK) ids[Tl::LEAD] = block_id(j + Tl::LEAD + 1);
+    }
+    // copies in flight land before the CTA can exit
+    if (lane == 0) {
+      mbar_wait_bounded(q_full, 0);
+      for (int kj = max(k_issued - Tl::KST, 0); kj < k_issued; ++kj)
+        mbar_wait_bounded(&k_full[kj % Tl::KST], (kj / Tl::KST) & 1);
+      for (int vj = max(v_issued - Tl::VST, 0); vj < v_issued; ++vj)
+        mbar_wait_bounded(&v_full[vj % Tl::VST], (vj / Tl::VST) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kIssuer) {
+    // ---------------- MMA issuer (lane 0), V tail zeroing (whole warp) ----------------
+    constexpr int fmt = LO ? 1 : 0;
+    constexpr uint32_t idesc_s = tc::instr_desc_f16(fmt, 0, 0, Tl::BM, BN);
+    constexpr uint32_t idesc_o = tc::instr_desc_f16(fmt, 0, 1, Tl::BM, D);
+    const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
+    auto issue_s = [&](int t, int j) {  // S_t = Q K_j^T
+      const uint32_t qb = aQ + (KSPLIT ? 0 : t) * Tl::Q_BYTES;
+      const uint32_t kb = aK + (j % Tl::KST) * Tl::KV_BYTES;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const uint32_t off = (s >> 2) * Tl::CB_BYTES + (s & 3) * 32;
+        tc::mma_ss(tmem + t * 256, tc::smem_desc_sw128(qb + off, 16, 1024),
+                   tc::smem_desc_sw128(kb + off, 16, 1024), idesc_s, s > 0);
+      }
+      tc::commit(&s_full[t]);
+    };
+    auto issue_pv = [&](int t, int st, bool accumulate) {  // O_t += P_t V
+      const uint32_t vb = aV + st * Tl::KV_BYTES;
+      const uint32_t tS = tmem + t * 256, tO = tS + 128;
+#pragma unroll
+      for (int s = 0; s < BN / 16; ++s) {
+        const uint64_t bdesc = tc::smem_desc_sw128(vb + s * 16 * 128, Tl::CB_BYTES, 1024);
+        const uint32_t pa = tS + 32 * (s >> 1) + 8 * (s & 1);  // keys 16s .. 16s + 15
+        tc::mma_ts(tO, pa, bdesc, idesc_o, accumulate || s > 0);
+        if constexpr (LO) tc::mma_ts(tO, pa + 16, bdesc, idesc_o, true);
+      }
+    };
+    auto k_ready = [&](int j) {
+      const bool r = wait_warp(&k_full[j % Tl::KST], (j / Tl::KST) & 1, abort_flag);
+      tc::fence_after_sync();
+      return r;
+    };
+    bool ok = wait_warp(q_full, 0, abort_flag) && k_ready(0);
+    if (ok) {
+      if (lane == 0) {
+        for (int t = 0; t < nq; ++t) issue_s(t, 0);
+        tc::commit(&k_empty[0]);
+      }
+      if (KSPLIT && NK > 1) {
+        ok = k_ready(1);
+        if (ok && lane == 0) {
+          issue_s(1, 1);
+          tc::commit(&k_empty[1 % Tl::KST]);
+        }
+      }
+    }
+    for (int j = 0; ok && j < NK; ++j) {
+      const int st = j % Tl::VST;
+      ok = wait_warp(&v_full[st], (j / Tl::VST) & 1, abort_flag);
+      if (!ok) break;
+      const int kb = t_beg + j * BN;
+      if (kb + BN > t_end) {
+        // keys past the end: P is 0 there, and 0 * NaN would not be
+        uint8_t* vs = sV + st * Tl::KV_BYTES;
+        for (int r = t_end - kb + lane; r < BN; r += 32)
+#pragma unroll
+          for (int c = 0; c < Tl::COLB; ++c)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              reinterpret_cast<uint4*>(vs + c * Tl::CB_BYTES + r * 128)[k] = make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if constexpr (KSPLIT) {
+        const int t = j & 1;
+        ok = wait_warp(&p_full[t], (j >> 1) & 1, abort_flag);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (lane == 0) {
+          issue_pv(t, st, j > 1);
+          if (j + 2 >= NK) tc::commit(&o_done[t]);
+          tc::commit(&v_empty[st]);
+        }
+        if (j + 2 < NK) {
+          ok = k_ready(j + 2);
+          if (!ok) break;
+          if (lane == 0) {
+            issue_s(t, j + 2);
+            tc::commit(&k_empty[(j + 2) % Tl::KST]);
+          }
+        }
+      } else {
+        for (int t = 0; ok && t < nq; ++t) {
+          ok = wait_warp(&p_full[t], j & 1, abort_flag);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (lane == 0) {
+            issue_pv(t, st, j > 0);
+            if (j == NK - 1) tc::commit(&o_done[t]);
+          }
+          if (j + 1 < NK) {
+            ok = k_ready(j + 1);
+            if (!ok) break;
+            if (lane == 0) issue_s(t, j + 1);
+          }
+        }
+        if (ok && lane == 0) {
+          tc::commit(&v_empty[st]);
+          if (j + 1 < NK) tc::commit(&k_empty[(j + 1) % Tl::KST]);
+        }
+      }
+    }
+    // every MMA issued has completed before tensor memory is released
+    if (lane == 0) {
+      tc::commit(mma_done);
+      mbar_wait_bounded(mma_done, 0);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax: warps 8t .. 8t + 7 serve stream t; warpgroup half
+    // hw of them takes keys 64 hw .. 64 hw + 63 of each key tile and output
+    // columns hw D / 2 .. of each row; thread r of a warpgroup owns row r ----------------
+    constexpr int HK = BN / 2;  // keys per half
+    constexpr int HD = D / 2;   // output columns per half
+    const int t = warp >> 3;
+    const int hw = (warp >> 2) & 1;
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tT = tmem + t * 256 + lane_base;
+    const uint32_t tS = tT + hw * HK, tO = tT + 128 + hw * HD;
+    const bool row_on = r < nrow[t];
+    const bool warp_on = (warp & 3) * 32 < nrow[t];  // a warp without rows only keeps step
+    const int rtok = r / G;
+    const int tok = q0 + tok0 + (KSPLIT ? 0 : t * qpt) + rtok;  // this row's query token
+    const int head = hk * G + (r - rtok * G);
+    int lim = t_end;  // this row sees the keys below
+    if (p.shared_lens && row_on)
+      lim = min(lim, shared_part(p.shared_lens[tok], p.lens[tok], p.L_cap, S));
+    float m = -INFINITY, l = 0.f;  // l: this half's share of the running sum
+    bool ok = nk[t] > 0;
+    const int nkt = nk[t];
+    auto slot = [&](int j, int half) { return xch + ((t * 2 + (j & 1)) * 2 + half) * Tl::BM; };
+    for (int j = 0; ok && j < nkt; ++j) {
+      ok = wait_warp(&s_full[t], j & 1, abort_flag);
+      if (!ok) break;
+      if (!warp_on) {  // (one arrival per phase: it waits for the phase it arrived at)
+        mbar_arrive(&xch_bar[t]);
+        ok = wait_warp(&xch_bar[t], j & 1, abort_flag);
+        if (!ok) break;
+        mbar_arrive(&p_full[t]);
+        continue;
+      }
+      tc::fence_after_sync();
+      const int kb = t_beg + (KSPLIT ? 2 * j + t : j) * BN + hw * HK;
+      float x[HK];
+      {
+        uint32_t u[HK];
+#pragma unroll
+        for (int c4 = 0; c4 < HK / 32; ++c4)
+          tc::tmem_ld32(tS + c4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c4 * 32]));
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < HK; ++c) x[c] = __uint_as_float(u[c]);
+        if (kb + HK > lim) {  // only tiles that reach past the row's last key pay for the mask
+#pragma unroll
+          for (int c = 0; c < HK; ++c) x[c] = kb + c >= lim ? -INFINITY : x[c];
+        }
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < HK; c += 2) mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], x[c], x[c + 1]);
+      const float hmax = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+      // the row's max over both halves (slots alternate with the key tile, so a
+      // half never overwrites a value the other has not read yet)
+      slot(j, hw)[r] = hmax;
+      mbar_arrive(&xch_bar[t]);
+      ok = wait_warp(&xch_bar[t], j & 1, abort_flag);
+      if (!ok) break;
+      const float tmax = fmaxf(hmax, slot(j, hw ^ 1)[r]) * p.scale_log2;
+      // The reference max only moves when the tile max exceeds it by more than
+      // 2^8 in weight; the weights stay <= 256, exact in the final ratio.
+      const float m_new = fmaxf(m, tmax);
+      const bool grow = m_new > m + 8.f;
+      const float m_use = grow ? m_new : m;
+      const float alpha = grow ? fast_exp2(m - m_use) : 1.f;
+      m = m_use;
+      // a row without keys so far keeps m = -inf; its weights are 2^-inf = 0
+      const float m_ref = m_use == -INFINITY ? 0.f : m_use;
+      // P over this half's scores, 8 keys at a time: keys 2k, 2k+1 of a 32-key
+      // chunk q as one 16-bit pair in column 32q + k, and for bf16 the rounding
+      // residue p - bf16(p), itself rounded, in column 32q + 16 + k
+      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+      const float2 nm2 = make_float2(-m_ref, -m_ref);
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int g = 0; g < HK / 8; ++g) {
+        float* v = &x[8 * g];
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 tt = ffma2(make_float2(v[2 * e], v[2 * e + 1]), sc2, nm2);
+          const float2 pe = make_float2(fast_exp2(tt.x), fast_exp2(tt.y));
+          acc[e & 1] = fadd2(acc[e & 1], pe);
+          hi[e] = pack_pair<T>(pe.x, pe.y);
+          if constexpr (LO) {
+            // bf16 pair -> the two fp32 values it holds: exact bit moves
+            const float2 hh = make_float2(__uint_as_float(hi[e] << 16),
+                                          __uint_as_float(hi[e] & 0xffff0000u));
+            lo[e] = pack_pair<T>(pe.x - hh.x, pe.y - hh.y);
+          }
+        }
+        const uint32_t col = 32 * (g >> 2) + 4 * (g & 3);  // within this half's 64 columns
+        tc::tmem_st4(tS + col, hi);
+        if constexpr (LO) tc::tmem_st4(tS + col + 16, lo);
+      }
+      // The stream's previous product has completed (the commit that released
+      // these scores covers it): rescale the rows whose max moved.
+      if (j > 0 && __any_sync(kFullMask, grow)) {
+#pragma unroll 1
+        for (int c4 = 0; c4 < HD / 32; ++c4) {
+          uint32_t u[32];
+          tc::tmem_ld32(tO + c4 * 32, u);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * alpha);
+          tc::tmem_st32(tO + c4 * 32, u);
+        }
+      }
+      l = l * alpha + ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y));
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      mbar_arrive(&p_full[t]);
+    }
+    // the row's sum over both halves
+    if (ok) {
+      slot(nkt, hw)[r] = l;
+      mbar_arrive(&xch_bar[t]);
+      ok = wait_warp(&xch_bar[t], nkt & 1, abort_flag);
+    }
+    if (ok) l += slot(nkt, hw ^ 1)[r];
+    if (ok) ok = wait_warp(&o_done[t], 0, abort_flag);
+    float w0 = 1.f, w1 = 0.f;  // weights of this stream's result and of the other's
+    float* jO = reinterpret_cast<float*>(sK);   // [D][128] stream 1's output, by column
+    float* jml = reinterpret_cast<float*>(sV);  // [2][128] its m and l
+    if constexpr (KSPLIT) {
+      // Stream 1 leaves its result in the rings' memory once both streams' MMAs
+      // are done with them; stream 0 joins it to its own.
+      if (t == 1 && ok) ok = wait_warp(&o_done[0], 0, abort_flag);
+      if (t == 1 && ok && warp_on) {
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int c4 = 0; c4 < HD / 32; ++c4) {
+          uint32_t u[32];
+          tc::tmem_ld32(tO + c4 * 32, u);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            jO[(hw * HD + c4 * 32 + c) * 128 + r] = __uint_as_float(u[c]);
+        }
+        if (hw == 0) {
+          jml[r] = m;
+          jml[128 + r] = l;
+        }
+      }
+      asm volatile("bar.sync 1, 512;" ::: "memory");  // every softmax thread, aborted or not
+      if (t == 1) ok = false;
+      if (ok && nk[1] > 0) {
+        const float m1 = jml[r], l1 = jml[128 + r];
+        const float M = fmaxf(m, m1);
+        w0 = m == -INFINITY ? 0.f : fast_exp2(m - M);
+        w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
+        l = w0 * l + w1 * l1;
+        m = M;
+      }
+    }
+    if (ok && warp_on) {
+      tc::fence_after_sync();
+      const int64_t ih = static_cast<int64_t>(tok) * p.H + head;
+      const float inv = direct ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      const float f0 = w0 * inv, f1 = w1 * inv;
+      const bool join = KSPLIT && nk[NST - 1] > 0;
+#pragma unroll 1
+      for (int c4 = 0; c4 < HD / 32; ++c4) {
+        uint32_t u[32];
+        tc::tmem_ld32(tO + c4 * 32, u);
+        tc::tmem_wait_ld();
+        float v[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(u[c]) * f0;
+        if (join) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            v[c] = fmaf(jO[(hw * HD + c4 * 32 + c) * 128 + r], f1, v[c]);
+        }
+        if (row_on) {
+          if (direct)
+            store_out32(p.out, p.out_dt, ih * D + hw * HD + c4 * 32, v);
+          else
+            store_row32<float>(p.ws_acc + (ih * p.NP + part) * D + hw * HD + c4 * 32, v);
+        }
+      }
+      if (!direct && hw == 0 && row_on) {
+        p.ws_m[ih * p.NP + part] = m;
+        p.ws_l[ih * p.NP + part] = l;
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kIssuer) {
+    __syncwarp();
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, Tl::TMEM_COLS);
+  }
+}
+
+// ---- merges ---------------------------------------------------------------------
+
+// The log-sum-exp join of one (row, head)'s results, by one warp: slots
+// a0 .. a0 + na - 1 and b0 .. b0 + nb - 1 (in that order) of its NP,
+//   M = max m;  out = sum 2^(m - M) acc / sum 2^(m - M) l;  all zero without any.
+template <int D>
+__device__ __forceinline__ void merge_row(const float* ws_m, const float* ws_l,
+                                          const float* ws_acc, int64_t ih, int NP, int a0, int na,
+                                          int b0, int nb, void* out, pa_dtype out_dt, int lane) {
+  constexpr int DL = D / 32;
+  const float* m = ws_m + ih * NP;
+  const float* l = ws_l + ih * NP;
+  const float* acc = ws_acc + ih * NP * D + lane * DL;
+  const int n = na + nb;
+  auto slot_of = [&](int q) { return q < na ? a0 + q : b0 + (q - na); };
+  float M = -INFINITY;
+  for (int q = lane; q < n; q += 32) M = fmaxf(M, m[slot_of(q)]);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+  float lsum = 0.f, a[DL];
+#pragma unroll
+  for (int e = 0; e < DL; ++e) a[e] = 0.f;
+  for (int c = 0; c < n; c += 32) {
+    const int q = c + lane;
+    float wq = 0.f;
+    if (q < n) {
+      const float mq = m[slot_of(q)];
+      wq = mq == -INFINITY ? 0.f : exp2f(mq - M);
+      lsum = fmaf(wq, l[slot_of(q)], lsum);
+    }
+    const int lim = min(32, n - c);
+#pragma unroll 4
+    for (int r = 0; r < lim; ++r) {
+      const float w = __shfl_sync(kFullMask, wq, r);
+      const float* row = acc + static_cast<int64_t>(slot_of(c + r)) * D;
+#pragma unroll
+      for (int e = 0; e < DL; e += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(row + e);
+        a[e] = fmaf(w, v.x, a[e]);
+        a[e + 1] = fmaf(w, v.y, a[e + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) lsum += __shfl_xor_sync(kFullMask, lsum, o);
+  const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+  const int64_t at = ih * D + lane * DL;
+#pragma unroll
+  for (int e = 0; e < DL; ++e) {
+    const float o = lsum > 0.f ? a[e] * inv : 0.f;
+    if (out_dt == PA_F32)
+      static_cast<float*>(out)[at + e] = o;
+    else if (out_dt == PA_BF16)
+      static_cast<__nv_bfloat16*>(out)[at + e] = __float2bfloat16_rn(o);
+    else
+      static_cast<__half*>(out)[at + e] = __float2half_rn(o);
+  }
+}
+
+// pa_cross: joins the partitions of the requests that have more than one. Grid:
+// (warps of (row, head) pairs, request).
+template <int D>
+__global__ void __launch_bounds__(128) cross_merge_kernel(const RowsParams p) {
+  const int lane = threadIdx.x & 31;
+  const int i = blockIdx.y;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int q0 = p.start[i], q1 = p.start[i + 1];
+  int L = p.lens[i];
+  grid_dependency_wait();
+  const int n = q1 - q0;
+  if (n < 0 || q0 < 0 || q1 > p.T || n > p.max_rows) return;
+  L = max(0, min(L, p.L_cap));
+  const int parts = static_cast<int>((static_cast<int64_t>(L) + p.P - 1) / p.P);
+  if (parts <= 1 || w >= static_cast<int64_t>(n) * p.H) return;
+  merge_row<D>(p.ws_m, p.ws_l, p.ws_acc, static_cast<int64_t>(q0) * p.H + w, p.NP, 0, parts, 0, 0,
+               p.out, p.out_dt, lane);
+}
+
+}  // namespace pa
