@@ -446,63 +446,69 @@ def pa_noalloc_scratch_bytes():
 PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN, PA_ROPE_BANDS = range(5)
 
 
-class _Here:
-    """The guard of a call whose tensors are on the current device."""
+# (These checks run at every call, some of which take a few microseconds: names are constant
+# tuples, devices compare as integers, and messages are made only where a check fails.)
 
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE_GUARD = _Here()
-
-
-def _on_device(named):
-    """Checks that the tensors are CUDA tensors of one device and returns a guard under which that
-    device is current (the call's stream defaults to its current stream)."""
-    dev = None
-    for name, t in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the others on {dev}")
-    return _HERE_GUARD if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _one_device(names, tensors):
+    """The index of the CUDA device that all the tensors (None: not given) are on."""
+    idx = -2
+    for n, t in enumerate(tensors):
+        if t is not None:
+            i = t.get_device()
+            if i != idx:
+                if i < 0:
+                    raise ValueError(f"{names[n]} must be a CUDA tensor")
+                if idx >= 0:
+                    raise ValueError(f"{names[n]} is on cuda:{i}, the others on cuda:{idx}")
+                idx = i
+    return idx
 
 
-def _contiguous(named):
-    for name, t in named:
+def _all_contiguous(names, tensors):
+    for n, t in enumerate(tensors):
         if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+            raise ValueError(f"{names[n]} must be contiguous")
 
 
-def _of_type(named, dtype):
-    for name, t in named:
+def _of_type(names, tensors, dtype):
+    for n, t in enumerate(tensors):
         if t is not None and t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}".replace("torch.", ""))
+            raise ValueError(f"{names[n]} must be {dtype}".replace("torch.", ""))
 
 
 def _half_type(t, name):
-    if t.dtype not in (torch.float16, torch.bfloat16):
+    dt = t.dtype
+    if dt != torch.bfloat16 and dt != torch.float16:
         raise ValueError(f"{name} must be float16 or bfloat16")
-    return t.dtype
+    return dt
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(name, idx, stream, *args):
+    """The entry point `name` on device `idx`: on `stream`, or that device's current stream."""
+    fn = getattr(lib(), name)
+    raw = torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == idx:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(idx):
+            rc = fn(*args, raw)
+    if rc != PA_OK:
+        raise PagedAttnError(rc, name)
 
 
 def _token_stride(t, name):
     """Elements from one token's rows to the next's of t [T, heads, D], heads contiguous."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [T, heads, D]")
-    if t.numel() == 0:
-        return t.shape[1] * t.shape[2]
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    T, heads, D = t.shape
+    if T == 0 or heads == 0:
+        return heads * D
+    step, head, one = t.stride()
+    if one != 1 or (head != D and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    # (one token has no next one)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return step if T > 1 else heads * D  # (one token has no next one)
 
 
 def pa_rope_table(rot_dim, base=10000.0, scaling=PA_ROPE_PLAIN, factor=1.0, low=1.0, high=32.0,
@@ -518,25 +524,31 @@ def pa_rope_table(rot_dim, base=10000.0, scaling=PA_ROPE_PLAIN, factor=1.0, low=
     return table, amplitude.value
 
 
-def _rope_common(q, k, positions, table, q_weight, k_weight, more):
-    """Checks shared by the pa_rope calls; returns (guard, T, H, Hkv, D)."""
-    guard = _on_device((("q", q), ("k", k), ("positions", positions), ("table", table),
-                        ("q_weight", q_weight), ("k_weight", k_weight)) + more)
+_ROPE_NAMES = ("positions", "table", "q_weight", "k_weight", "q", "k", "q_out", "k_out")
+_APPEND_NAMES = ("positions", "table", "q_weight", "k_weight", "slot_mapping", "k_cache",
+                 "v_cache", "q", "k", "q_out", "v")
+
+
+def _rope_common(q, k, q_out, positions, table, q_weight, k_weight):
+    """Checks shared by the pa_rope calls; returns (dtype, T, H, Hkv, D)."""
     dt = _half_type(q, "q")
-    _of_type((("k", k), ("q_weight", q_weight), ("k_weight", k_weight)), dt)
-    _of_type((("positions", positions),), torch.int32)
-    _of_type((("table", table),), torch.float64)
-    _contiguous((("positions", positions), ("table", table), ("q_weight", q_weight),
-                 ("k_weight", k_weight)))
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+    _of_type(("k", "q_out", "q_weight", "k_weight"), (k, q_out, q_weight, k_weight), dt)
+    if positions.dtype != torch.int32:
+        raise ValueError("positions must be int32")
+    if table.dtype != torch.float64:
+        raise ValueError("table must be float64")
+    if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [T, H, D] and k [T, Hkv, D]")
     T, H, D = q.shape
+    Tk, Hkv, Dk = k.shape
+    if Tk != T or Dk != D or q_out.shape != q.shape:
+        raise ValueError("q and q_out must be [T, H, D] and k [T, Hkv, D]")
     if positions.shape != (T,) or table.dim() != 1:
         raise ValueError("positions must be [T] and table [rot_dim / 2]")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and w.shape != (D,):
-            raise ValueError(f"{name} must be [D]")
-    return guard, T, H, k.shape[1], D
+    if (q_weight is not None and q_weight.shape != (D,)) or \
+            (k_weight is not None and k_weight.shape != (D,)):
+        raise ValueError("q_weight and k_weight must be [D]")
+    return dt, T, H, Hkv, D
 
 
 def pa_rope(q_out, k_out, q, k, positions, table, interleaved=False, amplitude=1.0, q_weight=None,
@@ -544,47 +556,44 @@ def pa_rope(q_out, k_out, q, k, positions, table, interleaved=False, amplitude=1
     """Norms (where a weight [D] is given) and rotates q [T, H, D] and k [T, Hkv, D] at
     positions [T] (int32) into q_out, k_out (which may be q, k). Tokens may be strided, heads are
     contiguous; table: float64 [rot_dim / 2] on the device (pa_rope_table)."""
-    guard, T, H, Hkv, D = _rope_common(q, k, positions, table, q_weight, k_weight,
-                                       (("q_out", q_out), ("k_out", k_out)))
-    _of_type((("q_out", q_out), ("k_out", k_out)), q.dtype)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("q_out and k_out must have the shapes of q and k")
-    with guard:
-        _check(lib().pa_rope(
-            _ptr(q_out), _token_stride(q_out, "q_out"), _ptr(k_out), _token_stride(k_out, "k_out"),
-            _ptr(q), _token_stride(q, "q"), _ptr(k), _token_stride(k, "k"), _ptr(positions),
-            _ptr(table), 2 * table.numel(), int(bool(interleaved)), float(amplitude),
-            _ptr(q_weight), _ptr(k_weight), float(eps), T, H, Hkv, D, _DT[q.dtype],
-            _stream(stream)), "pa_rope")
+    tensors = (positions, table, q_weight, k_weight, q, k, q_out, k_out)
+    idx = _one_device(_ROPE_NAMES, tensors)
+    _all_contiguous(_ROPE_NAMES, tensors[:4])
+    dt, T, H, Hkv, D = _rope_common(q, k, q_out, positions, table, q_weight, k_weight)
+    if k_out.dtype != dt or k_out.shape != k.shape:
+        raise ValueError("k_out must have k's type and shape")
+    _launch("pa_rope", idx, stream, q_out.data_ptr(), _token_stride(q_out, "q_out"),
+            k_out.data_ptr(), _token_stride(k_out, "k_out"), q.data_ptr(), _token_stride(q, "q"),
+            k.data_ptr(), _token_stride(k, "k"), positions.data_ptr(), table.data_ptr(),
+            2 * table.numel(), 1 if interleaved else 0, amplitude, _address(q_weight),
+            _address(k_weight), eps, T, H, Hkv, D, _DT[dt])
 
 
 def _rope_append(name, q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, scales, table,
                  interleaved, amplitude, q_weight, k_weight, eps, stream):
-    guard, T, H, Hkv, D = _rope_common(
-        q, k, positions, table, q_weight, k_weight,
-        (("q_out", q_out), ("v", v), ("slot_mapping", slot_mapping), ("k_cache", k_cache),
-         ("v_cache", v_cache)))
-    _of_type((("q_out", q_out), ("v", v)), q.dtype)
-    _of_type((("slot_mapping", slot_mapping),), torch.int64)
-    if scales:
-        if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
-            raise ValueError("E4M3 caches are uint8 tensors of codes")
-    else:
-        _of_type((("k_cache", k_cache), ("v_cache", v_cache)), q.dtype)
-    _contiguous((("slot_mapping", slot_mapping), ("k_cache", k_cache), ("v_cache", v_cache)))
-    if q_out.shape != q.shape or v.shape != k.shape or slot_mapping.shape != (T,):
-        raise ValueError("q_out must have q's shape, v k's, and slot_mapping must be [T]")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[1] != Hkv \
-            or k_cache.shape[3] != D:
+    tensors = (positions, table, q_weight, k_weight, slot_mapping, k_cache, v_cache, q, k, q_out, v)
+    idx = _one_device(_APPEND_NAMES, tensors)
+    _all_contiguous(_APPEND_NAMES, tensors[:7])
+    dt, T, H, Hkv, D = _rope_common(q, k, q_out, positions, table, q_weight, k_weight)
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be int64 [T]")
+    if v.dtype != dt or v.shape != k.shape:
+        raise ValueError("v must have k's type and shape")
+    cdt = torch.uint8 if scales else dt
+    if k_cache.dtype != cdt or v_cache.dtype != cdt:
+        raise ValueError("E4M3 caches are uint8 tensors of codes" if scales
+                         else "q, k, v and the caches must share one dtype")
+    if k_cache.dim() != 4:
         raise ValueError("the caches must be [NB, Hkv, S, D]")
-    NB, _, S, _ = k_cache.shape
-    with guard:
-        _check(getattr(lib(), name)(
-            _ptr(q_out), _token_stride(q_out, "q_out"), _ptr(q), _token_stride(q, "q"), _ptr(k),
-            _token_stride(k, "k"), _ptr(v), _token_stride(v, "v"), _ptr(positions),
-            _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(table),
-            2 * table.numel(), int(bool(interleaved)), float(amplitude), _ptr(q_weight),
-            _ptr(k_weight), float(eps), T, H, Hkv, D, S, NB, _DT[q.dtype], _stream(stream)), name)
+    NB, Hc, S, Dc = k_cache.shape
+    if Hc != Hkv or Dc != D or v_cache.shape != k_cache.shape:
+        raise ValueError("the caches must be [NB, Hkv, S, D]")
+    _launch(name, idx, stream, q_out.data_ptr(), _token_stride(q_out, "q_out"), q.data_ptr(),
+            _token_stride(q, "q"), k.data_ptr(), _token_stride(k, "k"), v.data_ptr(),
+            _token_stride(v, "v"), positions.data_ptr(), slot_mapping.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), *scales, table.data_ptr(), 2 * table.numel(),
+            1 if interleaved else 0, amplitude, _address(q_weight), _address(k_weight), eps, T, H,
+            Hkv, D, S, NB, _DT[dt])
 
 
 def pa_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, table,
@@ -602,19 +611,28 @@ def pa_rope_append_fp8(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache
                        eps=1e-6, stream=None):
     """pa_rope_append into uint8 E4M3 caches: codes of fp32(value / scale)."""
     _rope_append("pa_rope_append_fp8", q_out, q, k, v, positions, slot_mapping, k_cache, v_cache,
-                 (float(k_scale), float(v_scale)), table, interleaved, amplitude, q_weight,
-                 k_weight, eps, stream)
+                 (k_scale, v_scale), table, interleaved, amplitude, q_weight, k_weight, eps,
+                 stream)
 
 
-def _paged_common(out, q, k_cache, v_cache, block_tables, int32s, workspace):
-    """Checks shared by pa_cross and pa_decode_shared; returns the device guard."""
-    named = (("out", out), ("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-             ("block_tables", block_tables)) + int32s
-    guard = _on_device(named + (("workspace", workspace),))
-    _contiguous(named + (("workspace", workspace),))
+_CROSS_NAMES = ("out", "q", "k_cache", "v_cache", "block_tables", "workspace", "kv_lens",
+                "q_start")
+_SHARED_NAMES = ("out", "q", "k_cache", "v_cache", "block_tables", "workspace", "seq_lens",
+                 "shared_lens", "group_start")
+
+
+def _paged_common(names, tensors):
+    """Checks shared by pa_cross and pa_decode_shared (tensors in the order of their names);
+    returns (device index, workspace bytes)."""
+    idx = _one_device(names, tensors)
+    _all_contiguous(names, tensors)
+    out, q, k_cache, v_cache, block_tables, workspace = tensors[:6]
     dt = _half_type(q, "q")
-    _of_type((("k_cache", k_cache), ("v_cache", v_cache)), dt)
-    _of_type((("block_tables", block_tables),) + int32s, torch.int32)
+    if k_cache.dtype != dt or v_cache.dtype != dt:
+        raise ValueError("q and the caches must share one dtype")
+    if block_tables.dtype != torch.int32:
+        raise ValueError("block_tables must be int32")
+    _of_type(names[6:], tensors[6:], torch.int32)
     if out.dtype not in _DT:
         raise ValueError("out must be float32, float16 or bfloat16")
     if q.dim() != 3 or out.shape != q.shape:
@@ -623,11 +641,7 @@ def _paged_common(out, q, k_cache, v_cache, block_tables, int32s, workspace):
         raise ValueError("the caches must be [NB, Hkv, S, D]")
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be [B, MB]")
-    return guard
-
-
-def _ws_bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return idx, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def pa_cross_workspace_bytes(B, T, H, Hkv, D, max_q_len, max_kv_len, partition=0):
@@ -639,19 +653,17 @@ def pa_cross(out, q, k_cache, v_cache, block_tables, kv_lens, q_start, scale, ma
     """Cross attention over cached states: rows q_start[i] .. q_start[i + 1] - 1 of q [T, H, D]
     each see all kv_lens[i] tokens of block_tables[i]; caches [NB, Hkv, S, D]. workspace: a
     CUDA uint8 tensor of pa_cross_workspace_bytes(...) bytes, or None when that is 0."""
-    guard = _paged_common(out, q, k_cache, v_cache, block_tables,
-                          (("kv_lens", kv_lens), ("q_start", q_start)), workspace)
+    idx, ws_bytes = _paged_common(_CROSS_NAMES, (out, q, k_cache, v_cache, block_tables, workspace,
+                                                 kv_lens, q_start))
     T, H, D = q.shape
     NB, Hkv, S, _ = k_cache.shape
     B, MB = block_tables.shape
     if kv_lens.shape != (B,) or q_start.shape != (B + 1,):
         raise ValueError("kv_lens must be [B] and q_start [B + 1]")
-    with guard:
-        _check(lib().pa_cross(_ptr(out), _DT[out.dtype], _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                              _ptr(block_tables), MB, _ptr(kv_lens), _ptr(q_start), float(scale),
-                              B, H, Hkv, D, S, NB, _DT[q.dtype], T, int(max_q_len),
-                              int(max_kv_len), int(partition), _ptr(workspace),
-                              _ws_bytes(workspace), _stream(stream)), "pa_cross")
+    _launch("pa_cross", idx, stream, out.data_ptr(), _DT[out.dtype], q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), MB,
+            kv_lens.data_ptr(), q_start.data_ptr(), scale, B, H, Hkv, D, S, NB, _DT[q.dtype], T,
+            max_q_len, max_kv_len, partition, _address(workspace), ws_bytes)
 
 
 def pa_decode_shared_workspace_bytes(B, NG, H, Hkv, D, S, max_group, max_shared_len,
@@ -665,22 +677,19 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, seq_lens, shared_le
     """pa_decode_gqa's result for q, out [B, H, D] and caches [NB, Hkv, S, D], the first
     shared_lens[b] tokens of the requests of a group (group_start [NG + 1]) read once for the
     group. workspace: a CUDA uint8 tensor of pa_decode_shared_workspace_bytes(...) bytes."""
-    guard = _paged_common(out, q, k_cache, v_cache, block_tables,
-                          (("seq_lens", seq_lens), ("shared_lens", shared_lens),
-                           ("group_start", group_start)), workspace)
+    idx, ws_bytes = _paged_common(_SHARED_NAMES, (out, q, k_cache, v_cache, block_tables, workspace,
+                                                  seq_lens, shared_lens, group_start))
     B, H, D = q.shape
     NB, Hkv, S, _ = k_cache.shape
     if block_tables.shape[0] != B or seq_lens.shape != (B,) or shared_lens.shape != (B,) \
             or group_start.dim() != 1 or group_start.shape[0] < 1:
         raise ValueError("block_tables must be [B, MB], seq_lens and shared_lens [B], "
                          "group_start [NG + 1]")
-    with guard:
-        _check(lib().pa_decode_shared(
-            _ptr(out), _DT[out.dtype], _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-            block_tables.shape[1], _ptr(seq_lens), _ptr(shared_lens), _ptr(group_start),
-            group_start.shape[0] - 1, float(scale), B, H, Hkv, D, S, NB, _DT[q.dtype],
-            int(max_group), int(max_shared_len), int(max_tail_len), _ptr(workspace),
-            _ws_bytes(workspace), _stream(stream)), "pa_decode_shared")
+    _launch("pa_decode_shared", idx, stream, out.data_ptr(), _DT[out.dtype], q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], seq_lens.data_ptr(), shared_lens.data_ptr(),
+            group_start.data_ptr(), group_start.shape[0] - 1, scale, B, H, Hkv, D, S, NB,
+            _DT[q.dtype], max_group, max_shared_len, max_tail_len, _address(workspace), ws_bytes)
 
 
 def pa_copy_blocks(k_cache, v_cache, src_dst, stream=None):

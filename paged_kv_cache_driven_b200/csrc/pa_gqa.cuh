@@ -139,6 +139,13 @@ __device__ __forceinline__ float2 unpack2(uint32_t x) {
 // Prm = DecodeParamsTail: the tails of a batch with shared prefixes, the tokens
 // behind each request's shared part; every partition leaves its result in the
 // workspace.
+//
+// Prm = DecodeParamsFew: few packed query rows over whole key ranges (pa_cross, and
+// the shared part of pa_decode_shared): item i has the query tokens start[i] ..
+// start[i + 1] - 1, and its rows are (token, head of the KV head's group) pairs,
+// row r token r / G, head r % G; the columns of a CTA are up to 16 of them.
+// With the shared part of a group the keys are those of the longest shared
+// part among the CTA's requests, a column sees those of its own request.
 template <typename T, typename TO, int D, int S, bool APPEND, int NHT, typename TC = T,
           typename Prm = DecodeParams>
 __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
@@ -154,16 +161,41 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
   constexpr int SLAB = S * D * EB;
   constexpr int KS = D / 16;  // k-steps of S
 
+  constexpr bool FEW = std::is_same<Prm, DecodeParamsFew>::value;
   grid_dependents_launch();  // the merge of split requests may be scheduled early
   const int part = blockIdx.x;
   const int G = p.H / p.Hkv;
-  const int chunks = (G + 15) / 16;
-  const int hk = blockIdx.y / chunks;
-  const int c0 = (blockIdx.y % chunks) * 16;  // first query head (within the group) of this CTA
-  const int gc = min(16, G - c0);             // query heads served here
   const int i = blockIdx.z;
+  int rows = G;        // query rows of this KV head
+  int q0 = 0;          // FEW: the item's first query token
+  int most_rows = G;   // rows that the grid has CTAs for
+  if constexpr (FEW) {
+    q0 = __ldg(p.start + i);
+    const int q1 = __ldg(p.start + i + 1);
+    const int n = q1 - q0;
+    if (n < 0 || q0 < 0 || q1 > p.T || n > p.max_rows) {
+      if (threadIdx.x == 0 && part == 0 && blockIdx.y == 0) raise_error(PA_DEVERR_SEQ_LEN);
+      return;
+    }
+    rows = n * G;
+    most_rows = p.max_rows * G;
+  }
+  const int chunks = (most_rows + 15) / 16;
+  const int hk = blockIdx.y / chunks;
+  const int c0 = (blockIdx.y % chunks) * 16;  // first row (a query head of the group) of this CTA
+  const int gc = min(16, rows - c0);          // rows served here
+  if (FEW && gc <= 0) return;
   const int lane = threadIdx.x & 31;
   const int w = threadIdx.x >> 5;
+  // a row's place among the rows of q, out and the workspace
+  auto row_index = [&](int row) {
+    if constexpr (FEW) {
+      const int tok = (c0 + row) / G;
+      return static_cast<int64_t>(q0 + tok) * p.H + hk * G + (c0 + row - tok * G);
+    } else {
+      return static_cast<int64_t>(i) * p.H + static_cast<int64_t>(hk) * G + c0 + row;
+    }
+  };
 
   // The producer's first table entries assume a whole partition (P / S
   // blocks, clipped to the table's row), so they are requested together with
@@ -173,7 +205,30 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
   const int32_t* trow = p.block_tables + static_cast<int64_t>(i) * p.MB;
   int width = p.MB;  // entries of the table row from trow on
   constexpr bool TAIL = std::is_same<Prm, DecodeParamsTail>::value;
-  int L = __ldg(p.seq_lens + i);
+  int L = 0;
+  bool grouped = false;  // FEW: the shared part of a group of requests
+  if constexpr (FEW) grouped = p.shared_lens != nullptr;
+  if (!grouped) L = __ldg(p.seq_lens + i);
+  if constexpr (FEW) {
+    if (grouped) {
+      // the longest shared part of the requests served here, through that request's table
+      int who = q0 + c0 / G;
+      const int tok = q0 + c0 / G + lane;
+      if (tok <= q0 + (c0 + gc - 1) / G) {
+        const int sh = __ldg(p.shared_lens + tok), len = __ldg(p.seq_lens + tok);
+        if (w == 0 && part == 0 && hk == 0 && (sh < 0 || sh > p.L_cap || len < 0))
+          raise_error(PA_DEVERR_SEQ_LEN);
+        L = shared_part(sh, len, p.L_cap, S);
+        who = tok;
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        const int e = __shfl_xor_sync(kFullMask, L, o), b = __shfl_xor_sync(kFullMask, who, o);
+        if (e > L || (e == L && b < who)) L = e, who = b;
+      }
+      trow = p.block_tables + static_cast<int64_t>(who) * p.MB;
+    }
+  }
   if constexpr (TAIL) {
     if (L > p.MB * S) {  // past the table's row
       if (threadIdx.x == 0 && part == 0 && blockIdx.y == 0) raise_error(PA_DEVERR_SEQ_LEN);
@@ -197,8 +252,8 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
     L = L < 0 ? 0 : p.L_cap;
   }
   const int nparts = (L + p.P - 1) / p.P;
-  if ((TAIL || part > 0) && part >= nparts) return;
-  const bool direct = !TAIL && nparts <= 1;
+  if ((TAIL || grouped || part > 0) && part >= nparts) return;
+  const bool direct = !TAIL && !grouped && nparts <= 1;
 
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -320,8 +375,7 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
       const int row = 8 * nt + g;
       const uint32_t* qrow = reinterpret_cast<const uint32_t*>(
           static_cast<const uint8_t*>(p.q) +
-          ((static_cast<int64_t>(i) * p.H + static_cast<int64_t>(hk) * G + c0 +
-            min(row, gc - 1)) * D) * 2);
+          (row_index(min(row, gc - 1)) * D) * 2);
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
         qb[nt][kk][0] = row < gc ? __ldg(qrow + kk * 8 + t) : 0u;
@@ -367,10 +421,8 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
       for (int c = 0; c < QC; ++c) {
         val[c] = make_uint4(0, 0, 0, 0);
         if (row < gc) {
-          const int64_t hq = static_cast<int64_t>(hk) * G + c0 + row;
           val[c] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
-                                                   ((static_cast<int64_t>(i) * p.H + hq) * D +
-                                                    (sub + 8 * c) * 8) * 2);
+                                                   (row_index(row) * D + (sub + 8 * c) * 8) * 2);
         }
         const uint32_t wv[4] = {val[c].x, val[c].y, val[c].z, val[c].w};
 #pragma unroll
@@ -404,9 +456,8 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
       const int row = idx / (D / 8), ch = idx % (D / 8);
       uint4 val = make_uint4(0, 0, 0, 0);
       if (row < gc) {
-        const int64_t hq = static_cast<int64_t>(hk) * G + c0 + row;
         val = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
-                                              ((static_cast<int64_t>(i) * p.H + hq) * D + ch * 8) * 2);
+                                              (row_index(row) * D + ch * 8) * 2);
       }
       *reinterpret_cast<uint4*>(qtile + row * Tg::QPITCH + ch * 16) = val;
     }
@@ -470,6 +521,24 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
       }
       qs[nt][c] = p.q_scale * down;
     }
+
+  // FEW, grouped: the keys below lim[nt][c] are column 8 nt + 2t + c's; the
+  // units that reach past the shortest (lim_min) are masked column by column
+  int lim[FEW ? NHT : 1][2] = {};
+  int lim_min = 0x7fffffff;
+  if constexpr (FEW) {
+    if (grouped) {
+#pragma unroll
+      for (int nt = 0; nt < NHT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int tok = q0 + (c0 + min(8 * nt + 2 * t + c, gc - 1)) / G;
+          lim[nt][c] = shared_part(__ldg(p.shared_lens + tok), __ldg(p.seq_lens + tok), p.L_cap, S);
+          lim_min = min(lim_min, lim[nt][c]);
+        }
+      lim_min = __reduce_min_sync(kFullMask, lim_min);
+    }
+  }
 
   for (int k = w; k < nunits; k += NC) {
     const int s = k % NS;
@@ -551,6 +620,13 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
           sc[e] = ok ? (sacc[nt][e] + sodd[nt][e]) * qs[nt][e & 1] : -INFINITY;
         else
           sc[e] = ok ? (sacc[nt][e] + sodd[nt][e]) * p.q_scale : -INFINITY;
+      }
+      if constexpr (FEW) {
+        if (t0 + ROWS > lim_min) {  // warp-uniform
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (t0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) sc[e] = -INFINITY;
+        }
       }
       float pr[4];
 #pragma unroll
@@ -666,8 +742,7 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
       wt[c] = mc == -INFINITY ? 0.f : exp2f(mc - M);
       lsum = fmaf(wt[c], mg[(c * ROWS + row) * (D + 2) + 1], lsum);
     }
-    const int64_t hq = static_cast<int64_t>(hk) * G + c0 + row;
-    const int64_t ih = static_cast<int64_t>(i) * p.H + hq;
+    const int64_t ih = row_index(row);
     int64_t wslot = ih * p.NP + part;  // this result's place in the workspace
     if constexpr (TAIL) wslot += p.part0;
     for (int d = lane; d < D; d += 32) {

@@ -12,18 +12,28 @@ namespace {
 
 template <typename T, int LAYOUT, int MODE, int LPR>
 pa_status launch(RopeParams prm, cudaStream_t stream) {
-  // One CTA per token where the tokens fill the GPU. Fewer tokens have their
-  // rows spread over up to two CTAs per SM, down to one row per thread.
+  // Tokens that fill the GPU go kRopeTokens (as many as leave four CTAs per SM,
+  // about 1,000 threads' rows each) to a CTA. Fewer tokens than two CTAs per
+  // SM have their rows spread over CTAs, down to one row per thread.
   constexpr int RPP = 256 / LPR;
+  const int64_t sms = sm_count();
   const int64_t most = ceil_div(prm.rows, RPP);
-  const int64_t want = ceil_div(2 * static_cast<int64_t>(sm_count()), prm.T);
-  int64_t chunks = std::max<int64_t>(1, std::min(most, want));
+  int64_t chunks = std::max<int64_t>(1, std::min(most, ceil_div(2 * sms, prm.T)));
   prm.chunk_rows = static_cast<int>(ceil_div(ceil_div(prm.rows, chunks), RPP) * RPP);
   chunks = ceil_div(prm.rows, prm.chunk_rows);
   prm.chunks = static_cast<int>(chunks);
-  // (chunks > 1 only where T is at most 2 CTAs per SM: the product stays small)
+  if (chunks == 1) prm.chunk_rows = prm.rows;
+  prm.toks = 1;
+  if (chunks == 1)
+    while (prm.toks < kRopeTokens && prm.toks * prm.rows < 16 * RPP &&
+           static_cast<int64_t>(prm.T) >= 2 * prm.toks * 4 * sms)
+      prm.toks *= 2;
+  // (rows < 16 RPP where toks > 1, so the numbers stay far below 2^16 and the
+  // multiplication divides exactly)
+  prm.row_magic = ((uint64_t{1} << 32) + prm.rows - 1) / prm.rows;
+  const int64_t groups = ceil_div(prm.T, prm.toks);
   rope_kernel<T, LAYOUT, MODE, LPR>
-      <<<static_cast<unsigned>(prm.T * chunks), 256, 0, stream>>>(prm);
+      <<<static_cast<unsigned>(groups * chunks), 256, 0, stream>>>(prm);
   return cuda_status();
 }
 

@@ -74,8 +74,10 @@ struct RopeParams {
   float eps, amplitude, k_scale, v_scale;
   int T, H, Hkv, D, rot, S;
   int rows;                   // rows per token: H + Hkv, + Hkv with the append
-  int chunks;                 // CTAs per token
-  int chunk_rows;             // rows per CTA
+  int chunks;                 // CTAs per token (1 where toks > 1)
+  int chunk_rows;             // rows per CTA and token
+  int toks;                   // tokens per CTA
+  uint64_t row_magic;         // ceil(2^32 / rows): n / rows = (n * row_magic) >> 32
 };
 
 // Attention of packed query rows over whole paged key ranges (pa_cross, and the
@@ -111,6 +113,16 @@ struct DecodeParamsTail : DecodeParams {
   int part0;
   int shared_cap;              // host bound on shared_lens
   int tail_parts;              // partitions in the grid
+};
+
+// Few packed query rows over whole key ranges, on the grouped-query kernel
+// (pa_cross with few rows, and the shared part of small groups).
+struct DecodeParamsFew : DecodeParams {
+  const int32_t* start;        // [items + 1] first query token of each item
+  const int32_t* shared_lens;  // null for pa_cross; shared: [T] (seq_lens [T] too)
+  int T;                       // query tokens
+  int max_rows;                // host bound on an item's query tokens
+  int items, parts;            // grid
 };
 
 namespace host {
@@ -194,6 +206,9 @@ pa_status launch_rope(const RopeParams& prm, pa_dtype dt, int interleaved, int m
 // (items of at most one row tile), else the same key tiles of two row tiles
 pa_status launch_rows(const RowsParams& prm, const void* q, pa_dtype dt, int D, bool split_keys,
                       cudaStream_t stream);                             // pa_k_rows.cu
+// at most 16 rows (tokens x heads of a group) per CTA
+pa_status launch_few(const DecodeParamsFew& prm, pa_dtype dt, pa_dtype out_dt, int D, int S,
+                     cudaStream_t stream);                              // pa_k_few.cu
 pa_status launch_cross_merge(const RowsParams& prm, int D, cudaStream_t stream);
 pa_status launch_tails(const DecodeParamsTail& prm, pa_dtype dt, int D, int S,
                        cudaStream_t stream);                            // pa_k_shared.cu
@@ -209,6 +224,7 @@ bool take_error_append(unsigned int* bits);
 bool take_error_rope(unsigned int* bits);
 bool take_error_rows(unsigned int* bits);
 bool take_error_shared(unsigned int* bits);
+bool take_error_few(unsigned int* bits);
 
 }  // namespace host
 }  // namespace pa

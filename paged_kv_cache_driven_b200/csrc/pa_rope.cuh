@@ -11,13 +11,14 @@
 // position of 10^6 would leave an angle with an error of some 0.06.
 //
 // A stream bound by HBM: each value is read once and written once, and a value's
-// work is a dozen instructions. One CTA takes the rows (or a run of them) of one
-// token, so the D / 2 sines and cosines are computed once per CTA and kept in
-// registers over its rows: a thread owns four pairs of a row, D / 8 threads a
-// row, 256 / LPR rows at a time. Pairs, not consecutive elements, are what a
-// thread owns: in the half layout it loads two 8-byte pieces rot_dim / 2
-// apart, which keeps both components of a pair in one thread (no exchange
-// between lanes); warps still read whole 128-byte lines.
+// work is a dozen instructions. One CTA takes up to 8 tokens (kRopeTokens) with
+// all their rows, or, of few tokens, a run of one token's rows. Their sines and
+// cosines are computed once, into shared memory, under the first rows' loads. A
+// thread owns four pairs of a row, LPR threads a row, 256 / LPR rows at a time,
+// and loads U rows ahead of the U rows that it works on. Pairs, not
+// consecutive elements, are what a thread owns: in the half layout it loads two
+// 8-byte pieces rot_dim / 2 apart, which keeps both components of a pair in
+// one thread (no exchange between lanes); warps still read whole lines.
 #pragma once
 
 #include "pa_device.cuh"
@@ -32,6 +33,8 @@ enum : int {
   kHalfAny = 2    // the same for any even rot: single elements
 };
 enum : int { kNoCache = 0, kCache16 = 1, kCache8 = 2 };
+
+constexpr int kRopeTokens = 8;  // most tokens of a CTA
 
 // A thread's 8 elements of a row, as they lie in memory: 4 pairs.
 struct PairFrag {
@@ -181,143 +184,163 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int pl, int rot, int D
   }
 }
 
-// One CTA per (token, run of chunk_rows rows). Rows of a token: H of q, Hkv of
-// k, and with a cache Hkv of v. LPR: threads per row, a power of two >= D / 8.
+// The rows of a token: H of q, Hkv of k, and with a cache Hkv of v. LPR:
+// threads per row, a power of two >= D / 8. A CTA's work is the rows row0 ..
+// row1 - 1 of `toks` tokens from token t0, numbered token after token; thread
+// group `sub` takes numbers sub, sub + RPP, ...
 template <typename T, int LAYOUT, int MODE, int LPR>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(256, 4) rope_kernel(const RopeParams p) {
   constexpr int RPP = 256 / LPR;  // rows the CTA takes at a time
-  constexpr int U = 4;            // rows a thread has in flight
-  __shared__ float2 cs[128];
-  const int t = blockIdx.x / p.chunks;
-  const int row0 = (blockIdx.x - t * p.chunks) * p.chunk_rows;
-  const int row1 = min(row0 + p.chunk_rows, p.rows);
+  constexpr int U = 2;            // passes a thread has in flight
+  constexpr int NP = LPR * 4;     // pairs of a row, rounded up
+  __shared__ __align__(16) float s_cos[kRopeTokens][NP], s_sin[kRopeTokens][NP];
+  __shared__ __align__(16) float s_wa[2][NP], s_wb[2][NP];  // norm weights by pair, q and k
+  __shared__ int64_t s_dst[kRopeTokens];      // cache element of (head 0, this token), or -1
+  const int D = p.D, rot = p.rot, half = p.rot >> 1;
+  const int grp = blockIdx.x / p.chunks;
+  const int row0 = (blockIdx.x - grp * p.chunks) * p.chunk_rows;
+  const int nrow = min(p.chunk_rows, p.rows - row0);
+  const int t0 = grp * p.toks;
+  const int ntok = min(p.toks, p.T - t0);
+  const int total = ntok * nrow;
   const int sub = threadIdx.x / LPR, pl = threadIdx.x % LPR;
-  const bool lane_on = pl * 8 < p.D;
-  const int D = p.D, rot = p.rot;
+  const bool lane_on = pl * 8 < D;
+  const uint16_t* q = static_cast<const uint16_t*>(p.q);
+  const uint16_t* k = static_cast<const uint16_t*>(p.k);
+  const uint16_t* v = static_cast<const uint16_t*>(p.v);
 
-  int64_t slot = 0;
-  if constexpr (MODE != kNoCache) {
-    slot = __ldg(p.slots + t);
-    if (slot >= p.n_slots) {
-      if (threadIdx.x == 0 && row0 == 0) raise_error(PA_DEVERR_SLOT);
-      slot = -1;
-    }
-  }
-  const int64_t blk = slot < 0 ? 0 : slot / p.S;
-  const int64_t off = slot < 0 ? 0 : slot - blk * p.S;
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + t * p.q_stride;
-  const uint16_t* k = static_cast<const uint16_t*>(p.k) + t * p.k_stride;
-  const uint16_t* v = static_cast<const uint16_t*>(p.v) + t * p.v_stride;
-  // kind of a row: 0 q, 1 k, 2 v; -1: nothing to do (past the end, or skipped)
-  auto kind_of = [&](int row) {
-    if (row >= row1 || !lane_on) return -1;
-    if (row < p.H) return 0;
-    if (MODE != kNoCache && slot < 0) return -1;
-    return row < p.H + p.Hkv ? 1 : 2;
+  // number -> token of the CTA and row (one token: no division)
+  auto split = [&](int n, int& tok, int& row) {
+    tok = p.toks > 1 ? static_cast<int>((static_cast<uint64_t>(n) * p.row_magic) >> 32) : 0;
+    row = row0 + n - tok * nrow;
+  };
+  auto load = [&](int n, PairFrag& f) {
+    if (n >= total || !lane_on) return;
+    int tok, row;
+    split(n, tok, row);
+    const int64_t t = t0 + tok;
+    const uint16_t* src = q + t * p.q_stride + static_cast<int64_t>(row) * D;
+    if (row >= p.H) src = k + t * p.k_stride + static_cast<int64_t>(row - p.H) * D;
+    if (MODE != kNoCache && row >= p.H + p.Hkv)
+      src = v + t * p.v_stride + static_cast<int64_t>(row - p.H - p.Hkv) * D;
+    f = load_pairs<LAYOUT>(src, pl, rot, D);
   };
 
-  float c[4], s[4];
-  float wa[2][4], wb[2][4];  // norm weights of this thread's pairs, q and k
-#pragma unroll 1
-  for (int base = row0; base < row1; base += U * RPP) {
-    PairFrag f[U];
+  PairFrag cur[U] = {};
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = base + u * RPP + sub;
-      const int kind = kind_of(row);
-      f[u].w[0] = f[u].w[1] = f[u].w[2] = f[u].w[3] = 0;
-      if (kind < 0) continue;
-      const uint16_t* src = kind == 0   ? q + row * D
-                            : kind == 1 ? k + (row - p.H) * D
-                                        : v + (row - p.H - p.Hkv) * D;
-      f[u] = load_pairs<LAYOUT>(src, pl, rot, D);
+  for (int u = 0; u < U; ++u) load(u * RPP + sub, cur[u]);
+
+  // the tokens' sines and cosines, their places in the cache, the norm weights
+  for (int x = threadIdx.x; x < ntok * half; x += 256) {
+    const int tok = x / half, j = x - tok * half;
+    const double turns = __ldg(p.table + j);
+    const double pos = static_cast<double>(__ldg(p.positions + t0 + tok));
+    const double r = fma(pos, turns, -rint(pos * turns));  // [-1/2, 1/2]
+    float sv, cv;
+    sincospif(2.f * static_cast<float>(r), &sv, &cv);
+    s_cos[tok][j] = cv * p.amplitude;
+    s_sin[tok][j] = sv * p.amplitude;
+  }
+  if (MODE != kNoCache && threadIdx.x < ntok) {
+    const int64_t slot = __ldg(p.slots + t0 + threadIdx.x);
+    int64_t dst = -1;
+    if (slot >= p.n_slots) {
+      if (row0 == 0) raise_error(PA_DEVERR_SLOT);
+    } else if (slot >= 0) {
+      const int64_t blk = slot / p.S;
+      dst = (blk * p.Hkv * p.S + (slot - blk * p.S)) * D;
     }
-    if (base == row0) {  // the token's sines and cosines, under the first loads
-      if (threadIdx.x < rot >> 1) {
-        const double turns = __ldg(p.table + threadIdx.x);
-        const double pos = static_cast<double>(__ldg(p.positions + t));
-        const double r = fma(pos, turns, -rint(pos * turns));  // [-1/2, 1/2]
-        float sv, cv;
-        sincospif(2.f * static_cast<float>(r), &sv, &cv);
-        cs[threadIdx.x] = make_float2(cv * p.amplitude, sv * p.amplitude);
-      }
-      if (lane_on) {
+    s_dst[threadIdx.x] = dst;
+  }
+  const bool q_norm = p.q_weight != nullptr, k_norm = p.k_weight != nullptr;
+  if (threadIdx.x < LPR && lane_on) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const void* wt = part == 0 ? p.q_weight : p.k_weight;
-          if (!wt) continue;
-          const PairFrag wf = load_pairs<LAYOUT>(static_cast<const uint16_t*>(wt), pl, rot, D);
-          unpack_pairs<T, LAYOUT>(wf, wa[part], wb[part]);
-        }
-      }
-      __syncthreads();
+    for (int part = 0; part < 2; ++part) {
+      const void* wt = part == 0 ? p.q_weight : p.k_weight;
+      if (!wt) continue;
+      float a[4], b[4];
+      unpack_pairs<T, LAYOUT>(load_pairs<LAYOUT>(static_cast<const uint16_t*>(wt), pl, rot, D), a,
+                              b);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int j = 4 * pl + e;
-        const float2 v2 = j < rot >> 1 ? cs[j] : make_float2(1.f, 0.f);
-        c[e] = v2.x;
-        s[e] = v2.y;
+        s_wa[part][4 * pl + e] = a[e];
+        s_wb[part][4 * pl + e] = b[e];
       }
     }
+  }
+  __syncthreads();
+  const float inv_d = 1.f / static_cast<float>(D);
+  const int64_t head_step = static_cast<int64_t>(p.S) * D;
+
+#pragma unroll 1
+  for (int base = sub; base - sub < total; base += U * RPP) {
+    PairFrag nxt[U] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(base + (U + u) * RPP, nxt[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int row = base + u * RPP + sub;
-      const int kind = kind_of(row);
+      const int n = base + u * RPP;
+      if (n - sub >= total) break;  // (the whole CTA's)
+      int tok, row;
+      split(n, tok, row);
+      const bool on = n < total && lane_on;
+      const bool is_q = row < p.H;
+      const bool is_v = MODE != kNoCache && row >= p.H + p.Hkv;
       float a[4], b[4];
-      unpack_pairs<T, LAYOUT>(f[u], a, b);
-      // the norm's sum over the row's threads (every lane takes the shuffles)
-      if (p.q_weight || p.k_weight) {
+      unpack_pairs<T, LAYOUT>(cur[u], a, b);
+      if (q_norm || k_norm) {  // the sum over the row's threads: every lane takes the shuffles
         float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
 #pragma unroll
         for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
-        const bool norm = kind == 0 ? p.q_weight != nullptr : kind == 1 && p.k_weight != nullptr;
-        if (norm) {
-          const float inv = 1.f / sqrtf(ss / static_cast<float>(D) + p.eps);
+        if (is_q ? q_norm : (k_norm && !is_v)) {
+          const float inv = rsqrtf(fmaf(ss, inv_d, p.eps));
+          const float4 wa = *reinterpret_cast<const float4*>(&s_wa[is_q ? 0 : 1][4 * pl]);
+          const float4 wb = *reinterpret_cast<const float4*>(&s_wb[is_q ? 0 : 1][4 * pl]);
+          a[0] *= inv * wa.x, a[1] *= inv * wa.y, a[2] *= inv * wa.z, a[3] *= inv * wa.w;
+          b[0] *= inv * wb.x, b[1] *= inv * wb.y, b[2] *= inv * wb.z, b[3] *= inv * wb.w;
+        }
+      }
+      if (!on) continue;
+      if (!is_v && 4 * pl < half) {
+        const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[tok][4 * pl]);
+        const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[tok][4 * pl]);
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[e] *= inv * (kind == 0 ? wa[0][e] : wa[1][e]);
-            b[e] *= inv * (kind == 0 ? wb[0][e] : wb[1][e]);
+        for (int e = 0; e < 4; ++e) {
+          // past the rotation pairs pass through (an infinity times a zero sine is no zero);
+          // in the vector half layout a thread's pairs are all on one side
+          if (LAYOUT == kHalf || 4 * pl + e < half) {
+            const float x = a[e], y = b[e];
+            a[e] = x * c[e] - y * s[e];
+            b[e] = y * c[e] + x * s[e];
           }
         }
       }
-      if (kind < 0) continue;
-      if (kind == 2) {  // values pass as they are
-        if constexpr (MODE != kNoCache) {
-          const int64_t dst = ((blk * p.Hkv + (row - p.H - p.Hkv)) * p.S + off) * D;
-          if constexpr (MODE == kCache16)
-            store_pairs<LAYOUT>(static_cast<uint16_t*>(p.v_cache) + dst, pl, rot, D, f[u]);
-          else
-            store_codes<LAYOUT>(static_cast<uint8_t*>(p.v_cache) + dst, pl, rot, D, a, b,
-                                p.v_scale);
-        }
-        continue;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (4 * pl + e < rot >> 1) {  // others pass through (an infinity times 0 is no 0)
-          const float x = a[e], y = b[e];
-          a[e] = x * c[e] - y * s[e];
-          b[e] = y * c[e] + x * s[e];
-        }
-      }
-      if (kind == 0 || MODE == kNoCache) {
-        uint16_t* dst = kind == 0
-                            ? static_cast<uint16_t*>(p.q_out) + t * p.q_out_stride + row * D
-                            : static_cast<uint16_t*>(p.k_out) + t * p.k_out_stride +
-                                  (row - p.H) * D;
+      if (MODE == kNoCache || is_q) {
+        const int64_t t = t0 + tok;
+        uint16_t* dst = static_cast<uint16_t*>(p.q_out) + t * p.q_out_stride +
+                        static_cast<int64_t>(row) * D;
+        if (!is_q)
+          dst = static_cast<uint16_t*>(p.k_out) + t * p.k_out_stride +
+                static_cast<int64_t>(row - p.H) * D;
         store_pairs<LAYOUT>(dst, pl, rot, D, pack_pairs<T, LAYOUT>(a, b));
-      } else {
-        const int64_t dst = ((blk * p.Hkv + (row - p.H)) * p.S + off) * D;
-        if constexpr (MODE == kCache16)
-          store_pairs<LAYOUT>(static_cast<uint16_t*>(p.k_cache) + dst, pl, rot, D,
-                              pack_pairs<T, LAYOUT>(a, b));
-        else if constexpr (MODE == kCache8)
-          store_codes<LAYOUT>(static_cast<uint8_t*>(p.k_cache) + dst, pl, rot, D, a, b,
-                              p.k_scale);
+      } else if constexpr (MODE != kNoCache) {
+        const int64_t at = s_dst[tok];
+        if (at < 0) continue;  // padding, or a slot past the cache
+        const int64_t dst = at + (row - p.H - (is_v ? p.Hkv : 0)) * head_step;
+        void* cache = is_v ? p.v_cache : p.k_cache;
+        if constexpr (MODE == kCache16)  // values pass bit for bit
+          store_pairs<LAYOUT>(static_cast<uint16_t*>(cache) + dst, pl, rot, D,
+                              is_v ? cur[u] : pack_pairs<T, LAYOUT>(a, b));
+        else
+          store_codes<LAYOUT>(static_cast<uint8_t*>(cache) + dst, pl, rot, D, a, b,
+                              is_v ? p.v_scale : p.k_scale);
       }
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) cur[u] = nxt[u];
   }
 }
 
