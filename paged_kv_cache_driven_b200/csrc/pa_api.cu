@@ -286,6 +286,21 @@ bool query_rows_map(CUtensorMap* out, const void* q, int64_t T, int H, int D, in
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool row_cols_map(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows,
+                  pa_dtype dt) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t cols = static_cast<cuuint32_t>(D / 64);
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), cols};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), cols};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(out, dt == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool row_map_now(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows,
                  pa_dtype dt) {
   return encode_row_map(out, base, rows, D, box_rows, dt == PA_BF16 ? 1 : 0);
@@ -982,19 +997,21 @@ RowsPlan plan_rows(int items, int max_rows, int G, int Hkv, int D, int max_len, 
   RowsPlan best{};
   double best_cost = 0.0;
   bool any = false;
-  for (int split = D == 256 ? 0 : 1; split >= 0; --split) {
-    const int row_tiles = (split || D == 256) ? 1 : 2;
+  // head size 64 has two CTAs of one row tile per SM, 256 one
+  const int64_t slots = D == 64 ? 2 * sms : sms;
+  for (int split = D == 128 ? 1 : 0; split >= 0; --split) {
+    const int row_tiles = (split || D != 128) ? 1 : 2;
     if (row_tiles == 2 && max_rows <= qpt) continue;  // nothing for the second half
     const double tile_cost = split ? 1.0 : 2.0;
     const int64_t ctas = static_cast<int64_t>(std::max(items, 1)) * Hkv *
                          std::max<int64_t>(1, ceil_div(max_rows, row_tiles * qpt));
     const int64_t most =
-        partition == 0 ? std::min(tiles, std::max<int64_t>(8, 2 * sms / ctas + 1)) : 1;
+        partition == 0 ? std::min(tiles, std::max<int64_t>(8, 2 * slots / ctas + 1)) : 1;
     for (int64_t c = 1; c <= most; ++c) {
       int64_t per = ceil_div(tiles, c);
       if (partition > 0) per = partition / kKeyTile;
       const int64_t parts = ceil_div(tiles, per);
-      const int64_t waves = ceil_div(ctas * parts, sms);
+      const int64_t waves = ceil_div(ctas * parts, slots);
       double cost = static_cast<double>(waves) * (per * tile_cost + 2.0);
       if (parts > 1)  // the merge: its launch, and its reads and writes of the results
         cost += 1.5 + static_cast<double>(items) * max_rows * Hkv * G * parts * D * 8.0 / 9.0e6;

@@ -22,7 +22,7 @@ pa_status launch(const RowsParams& prm, const void* q, cudaStream_t stream) {
   CUtensorMap tmq, tmk, tmv;
   if (!query_rows_map(&tmq, q, prm.T, prm.H, D, prm.H / prm.Hkv, prm.qpt, dt) ||
       !row_map_now(&tmk, prm.k_cache, rows, D, prm.S, dt) ||
-      !row_map_now(&tmv, prm.v_cache, rows, D, prm.S, dt))
+      !row_cols_map(&tmv, prm.v_cache, rows, D, prm.S, dt))
     return PA_ERR_CUDA;
   const int64_t groups = ceil_div(prm.max_rows, Tl::NQ * prm.qpt);
   const dim3 grid(static_cast<unsigned>(groups * prm.Hkv), prm.parts, prm.items);
@@ -32,7 +32,7 @@ pa_status launch(const RowsParams& prm, const void* q, cudaStream_t stream) {
 
 template <typename T>
 pa_status by_size(const RowsParams& prm, const void* q, int D, bool split_keys, cudaStream_t st) {
-  if (D == 64) return split_keys ? launch<T, 64, true>(prm, q, st) : launch<T, 64, false>(prm, q, st);
+  if (D == 64) return launch<T, 64, false>(prm, q, st);
   if (D == 128)
     return split_keys ? launch<T, 128, true>(prm, q, st) : launch<T, 128, false>(prm, q, st);
   if (D == 256) return launch<T, 256, false>(prm, q, st);

@@ -155,6 +155,10 @@ bool row_map(CUtensorMap* out, const void* base, int64_t rows, int D, int box_ro
 // row_map_now: the same, encoded anew at each call.
 bool row_map_now(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows,
                  pa_dtype dt);
+// row_cols_map: a cache as (64 elements, rows, D / 64 column blocks); a box is
+// box_rows rows of all column blocks, one 128-byte wide tile after the other.
+bool row_cols_map(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows,
+                  pa_dtype dt);
 // row_map_codes: the same view of a cache of one-byte E4M3 codes; a box is one
 // whole D-byte row x box_rows rows, unswizzled.
 bool row_map_codes(CUtensorMap* out, const void* base, int64_t rows, int D, int box_rows);

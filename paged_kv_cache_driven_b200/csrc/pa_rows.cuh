@@ -12,9 +12,8 @@
 // block (box 64 x G heads x qpt tokens), row r = token r / G, head r % G. K and V
 // are thus read once for all of a tile's tokens and heads.
 //
-// One CTA per (row tiles, KV head, partition of the keys, item), 576 threads (320
-// at head size 256) in the roles of the causal prefill kernel: two softmax
-// warpgroups per stream, a producer warp (one lane per cache block and TMA box),
+// One CTA per (row tiles, KV head, partition of the keys, item), up to 640 threads in the roles of the causal prefill kernel: two softmax
+// warpgroups per stream, producer warps (one lane per cache block and TMA box),
 // an MMA issuer warp that also owns tensor memory. Two streams ping-pong, so
 // that the tensor cores work for one while the other's softmax runs:
 //   KSPLIT = false  stream t takes row tile t: both read every key tile;
@@ -43,13 +42,23 @@ template <int D, bool KSPLIT>
 struct RowsTiling {
   static constexpr int BM = 128;              // query rows per tile (MMA M)
   static constexpr int BN = 128;              // keys per tile
-  // streams: two, or one at head size 256 (tensor memory and shared memory, as
-  // in the prefill kernel)
-  static constexpr int NST = D == 256 ? 1 : 2;
+  // Streams: two at head size 128. One at head size 256, which fills tensor and
+  // shared memory, and at head size 64, where two CTAs share an SM instead
+  // (256 tensor-memory columns and some 85 KB each) and also cover each other's
+  // start and end (16 ragged prompts on 32 heads: 115 us with two streams per CTA).
+  static constexpr int NST = D == 128 ? 2 : 1;
+  static constexpr int CTAS = D == 64 ? 2 : 1;  // per SM
   static constexpr int NQ = KSPLIT ? 1 : NST;  // query tiles held
-  static constexpr int KST = D == 256 ? 1 : (D == 128 ? 2 : 4);  // K stages
+  static constexpr int KST = D == 256 ? 1 : 2;  // K stages
   static constexpr int VST = KST;                                // V stages
-  static constexpr int LEAD = KSPLIT ? 2 : 1;  // key tiles K runs ahead of V
+  // Producer warps: a warp gets a TMA box out about every 90 cycles (one lane
+  // each; 180 from a single lane), so one warp with all 32 boxes of a K and a V
+  // tile in blocks of 16 held the pipeline at 3,300 cycles per key tile. K has
+  // NKP warps that share a tile's column blocks; V has one, whose boxes span all
+  // column blocks (V's tile may lie block by block: see dV; K's has to be whole
+  // columns of 128 rows).
+  // Two CTAs on an SM have one warp each for both operands (their registers).
+  static constexpr int NKP = D == 64 ? 1 : 2, NPROD = D == 64 ? 1 : NKP + 1;
   static constexpr int COLB = D / 64;
   static constexpr int CB_BYTES = 128 * 128;  // one column block of 128 rows
   static constexpr int Q_BYTES = BM * D * 2;
@@ -59,30 +68,143 @@ struct RowsTiling {
   static constexpr int OFF_XCH = OFF_V + VST * KV_BYTES;
   static constexpr int XCH_BYTES = NST * 2 * 2 * BM * 4;  // [stream][phase parity][half][row]
   static constexpr int OFF_BAR = OFF_XCH + XCH_BYTES;
-  // at least 120 KB, so that one CTA holds an SM (it allocates all 512
-  // tensor-memory columns)
-  static constexpr int SMEM = 1024 + OFF_BAR + 256 > 120 * 1024 ? 1024 + OFF_BAR + 256 : 120 * 1024;
-  static constexpr int THREADS = NST * 256 + 64;
-  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr int SMEM = 1024 + OFF_BAR + 256;
+  static constexpr int THREADS = NST * 256 + NPROD * 32 + 32;
+  static constexpr uint32_t TMEM_COLS = 512 / CTAS;
+  // an SM holds CTAS of these, no more: their tensor memory is what there is
+  static_assert((CTAS + 1) * SMEM > 232448, "CTAs per SM");
+  static_assert(CTAS * SMEM <= 232448 && 128 + D <= TMEM_COLS / NST, "CTAs per SM");
   static_assert(!KSPLIT || NST == 2, "two streams share the keys");
-  static_assert(KST >= LEAD || D == 256, "K runs LEAD tiles ahead");
-  static_assert(!KSPLIT || D * 128 * 4 <= KST * KV_BYTES, "the join's O fits the K ring");
+  static_assert(!KSPLIT || (D * 128 * 4 <= KST * KV_BYTES && 65536 <= VST * KV_BYTES),
+                "the join's exchange fits the rings");
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
-// 32 consecutive output elements of one row.
-__device__ __forceinline__ void store_out32(void* out, pa_dtype dt, int64_t at,
-                                            const float (&v)[32]) {
-  if (dt == PA_F32)
-    store_row32<float>(static_cast<float*>(out) + at, v);
-  else if (dt == PA_BF16)
-    store_row32<__nv_bfloat16>(static_cast<__nv_bfloat16*>(out) + at, v);
-  else
-    store_row32<__half>(static_cast<__half*>(out) + at, v);
+// ---- MMA issue by a whole warp ----------------------------------------------------
+// The issuing warp runs these with all its lanes, one elected lane's instruction
+// taking effect (`on`), and with descriptors that are a uniform base plus a
+// constant: the operands then stay in uniform registers. Issued from inside an
+// `if (lane == 0)`, with each descriptor put together from its fields, an MMA took
+// the issuing lane some 87 cycles, more than the tensor core needs for it.
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on;
+}
+
+__device__ __forceinline__ void mma_ss_on(uint32_t on, uint32_t d_tmem, uint64_t a_desc,
+                                          uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_ts_on(uint32_t on, uint32_t d_tmem, uint32_t a_tmem,
+                                          uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_on(uint32_t on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(on)
+      : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const void* tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+
+// One arrival for a whole warp (its lanes' earlier writes are ordered before it).
+__device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) {
+  tc::tmem_ld32(taddr, r);
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Stores 4 W bytes of each of a warp's 32 rows (lane r holds row r's W words; the
+// rows' destinations differ, rows from `rows` on are not stored) through 32 x W
+// words of shared memory, so that every store instruction writes whole
+// segments of 4 W bytes: stored from the row's own lane, each instruction would
+// touch 32 lines. 16-byte pieces are placed so that neither side conflicts.
+template <int W>
+__device__ __forceinline__ void store_rows(uint8_t* buf, const uint32_t (&w)[W], uint8_t* dst,
+                                           int rows, int lane) {
+  constexpr int NP = W / 4;  // 16-byte pieces per row
+  auto place = [](int row, int piece) {
+    const int x = W == 32 ? row & 7 : (W == 16 ? (row >> 1) & 3 : (row >> 2) & 1);
+    return row * W * 4 + ((piece ^ x) << 4);
+  };
+  __syncwarp();  // the warp's previous use of buf is over
+#pragma unroll
+  for (int k = 0; k < NP; ++k)
+    *reinterpret_cast<uint4*>(buf + place(lane, k)) =
+        make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  __syncwarp();
+  const int piece = lane % NP;
+#pragma unroll
+  for (int base = 0; base < 32; base += 32 / NP) {
+    const int row = base + lane / NP;
+    const uint64_t at = __shfl_sync(kFullMask, reinterpret_cast<uint64_t>(dst), row);
+    const uint4 x = *reinterpret_cast<const uint4*>(buf + place(row, piece));
+    if (row < rows) reinterpret_cast<uint4*>(at)[piece] = x;
+  }
+}
+
+// C consecutive output elements of each of a warp's rows, in the output's type.
+template <int C>
+__device__ __forceinline__ void store_out(uint8_t* buf, const float (&v)[C], void* out,
+                                          pa_dtype dt, int64_t at, int rows, int lane) {
+  if (dt == PA_F32) {
+    uint32_t w[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) w[c] = __float_as_uint(v[c]);
+    store_rows<C>(buf, w, reinterpret_cast<uint8_t*>(static_cast<float*>(out) + at), rows, lane);
+  } else {
+    uint32_t w[C / 2];
+#pragma unroll
+    for (int c = 0; c < C / 2; ++c)
+      w[c] = dt == PA_BF16 ? pack_pair<__nv_bfloat16>(v[2 * c], v[2 * c + 1])
+                           : pack_pair<__half>(v[2 * c], v[2 * c + 1]);
+    store_rows<C / 2>(buf, w, reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(out) + at), rows,
+                      lane);
+  }
 }
 
 template <typename T, int D, bool KSPLIT>
-__global__ void __launch_bounds__(576, 1)
+__global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, KSPLIT>::CTAS)
     rows_kernel(const RowsParams p, const __grid_constant__ CUtensorMap tmq,
                 const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv) {
@@ -101,6 +223,11 @@ __global__ void __launch_bounds__(576, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = p.S;
 
+  if (threadIdx.x == 0) {  // the tensor maps' first use then finds them cached
+    prefetch_map(&tmq);
+    prefetch_map(&tmk);
+    prefetch_map(&tmv);
+  }
   const int q0 = p.start[i], q1 = p.start[i + 1];
   const int n = q1 - q0;
   const bool first_cta = blockIdx.x == 0 && part == 0;
@@ -191,7 +318,8 @@ __global__ void __launch_bounds__(576, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   static_assert((1 + 2 * Tl::KST + 2 * Tl::VST + 4 * NST + 1) * 8 + 8 <= 256, "barriers");
 
-  constexpr int kProducer = 8 * NST, kIssuer = kProducer + 1;
+  constexpr int NKP = Tl::NKP, kProducer = 8 * NST, kIssuer = kProducer + Tl::NPROD;
+  const bool producer = warp >= kProducer && warp < kIssuer;
   const int bpt = BN / S;  // cache blocks per key tile
   const int blk0 = t_beg / S, nblk = (t_end + S - 1) / S;
   const int32_t* table = p.block_tables + static_cast<int64_t>(trow) * p.MB;
@@ -208,47 +336,66 @@ __global__ void __launch_bounds__(576, 1)
     }
     return id;
   };
-  // one K or V tile: every lane issues the boxes of its block
-  auto load_tile = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full, int id) {
+  // part of one K or V tile: every lane issues the boxes of its block (K: of the
+  // warp's column blocks; V: one of all column blocks)
+  const int col0 = (warp - kProducer) % NKP;
+  auto load_tile = [&](bool v, int j, int id) {
+    const int st = j % (v ? Tl::VST : Tl::KST);
+    uint8_t* dst = (v ? sV : sK) + st * Tl::KV_BYTES;
+    uint64_t* full = &(v ? v_full : k_full)[st];
     const int nvalid = __popc(__ballot_sync(kFullMask, id >= 0));
     if (lane == 0)
-      mbar_arrive_expect_tx(full, static_cast<uint32_t>(nvalid) * S * 128 * Tl::COLB);
+      mbar_arrive_expect_tx(full, static_cast<uint32_t>(nvalid) * S * 128 *
+                                      (v ? Tl::COLB : Tl::COLB / NKP));
     __syncwarp();
     if (id >= 0) {
       const int y = (id * p.Hkv + hk) * S;
+      if (v) {
+        tc::tma_load_3d(dst + lane * S * 128 * Tl::COLB, &tmv, 0, y, 0, full);
+      } else {
 #pragma unroll
-      for (int c = 0; c < Tl::COLB; ++c)
-        tma_load_2d_nohint(dst + c * Tl::CB_BYTES + lane * S * 128, map, c * 64, y, full);
+        for (int c = 0; c < Tl::COLB / NKP; ++c) {
+          const int col = col0 + c * NKP;
+          tma_load_2d_nohint(dst + col * Tl::CB_BYTES + lane * S * 128, &tmk, col * 64, y, full);
+        }
+      }
     }
   };
-  // The producer initialises the barriers and issues Q and the first K tiles
-  // before the CTA-wide sync, under the tensor-memory allocation.
-  int ids[Tl::LEAD + 1];  // block ids of key tiles j .. j + LEAD
-  if (warp == kProducer) {
-    if (lane == 0) {
+  // whether tile j's stage is free
+  auto stage_free = [&](bool v, int j) {
+    const int ns = v ? Tl::VST : Tl::KST;
+    return j < ns ||
+           wait_warp(&(v ? v_empty : k_empty)[j % ns], ((j / ns) - 1) & 1, abort_flag);
+  };
+  // The producers issue Q and the first tiles before the CTA-wide sync, under the
+  // tensor-memory allocation.
+  static_assert(Tl::KST == Tl::VST, "the first tiles");
+  constexpr bool one_warp = Tl::NPROD == 1;    // for both operands
+  const bool is_v = warp == kProducer + NKP;   // (not one_warp)
+  const int ahead = min(NK, Tl::KST);
+  int next_id = -1;
+  if (producer) {
+    if (warp == kProducer && lane == 0) {
       mbar_init(q_full, 1);
       for (int s = 0; s < Tl::KST; ++s) {
-        mbar_init(&k_full[s], 1);
+        mbar_init(&k_full[s], NKP);
         mbar_init(&k_empty[s], 1);
-      }
-      for (int s = 0; s < Tl::VST; ++s) {
         mbar_init(&v_full[s], 1);
         mbar_init(&v_empty[s], 1);
       }
       for (int t = 0; t < NST; ++t) {
         mbar_init(&s_full[t], 1);
-        mbar_init(&p_full[t], 256);
+        mbar_init(&p_full[t], 8);  // one arrival per softmax warp
         mbar_init(&o_done[t], 1);
-        mbar_init(&xch_bar[t], 256);
+        mbar_init(&xch_bar[t], 8);
       }
       mbar_init(mma_done, 1);
       *abort_flag = 0;
       fence_mbar_init();
     }
-    __syncwarp();
-#pragma unroll
-    for (int a = 0; a <= Tl::LEAD; ++a) ids[a] = a < NK ? block_id(a) : -1;
-    if (lane == 0) {
+    next_id = block_id(0);
+    asm volatile("bar.sync 2, %0;" ::"n"(Tl::NPROD * 32) : "memory");  // the barriers are there
+    if (warp == kProducer && lane == 0) {
       mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nq) * Tl::COLB * G * qpt * 128);
       for (int t = 0; t < nq; ++t)
 #pragma unroll
@@ -256,9 +403,12 @@ __global__ void __launch_bounds__(576, 1)
           tc::tma_load_3d(sQ + t * Tl::Q_BYTES + c * Tl::CB_BYTES, &tmq, c * 64, hk * G,
                           q0 + tok0 + t * qpt, q_full);
     }
-#pragma unroll
-    for (int a = 0; a < Tl::LEAD; ++a)
-      if (a < NK) load_tile(&tmk, sK + (a % Tl::KST) * Tl::KV_BYTES, &k_full[a % Tl::KST], ids[a]);
+    __syncwarp();
+    for (int j = 0; j < ahead; ++j) {
+      if (one_warp || !is_v) load_tile(false, j, next_id);
+      if (one_warp || is_v) load_tile(true, j, next_id);
+      if (j + 1 < NK) next_id = block_id(j + 1);
+    }
   }
   if (warp == kIssuer) {
     __syncwarp();
@@ -269,72 +419,69 @@ __global__ void __launch_bounds__(576, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  if (warp == kProducer) {
-    // ---------------- producer ----------------
-    int k_issued = min(NK, Tl::LEAD), v_issued = 0;
-    auto next_k = [&](int j) {  // K(j + LEAD)
-      const int kj = j + Tl::LEAD, st = kj % Tl::KST;
-      if (kj >= NK) return true;
-      if (kj >= Tl::KST && !wait_warp(&k_empty[st], ((kj / Tl::KST) - 1) & 1, abort_flag))
-        return false;
-      load_tile(&tmk, sK + st * Tl::KV_BYTES, &k_full[st], ids[Tl::LEAD]);
-      k_issued = kj + 1;
-      return true;
-    };
-    auto next_v = [&](int j) {
-      const int st = j % Tl::VST;
-      if (j >= Tl::VST && !wait_warp(&v_empty[st], ((j / Tl::VST) - 1) & 1, abort_flag))
-        return false;
-      load_tile(&tmv, sV + st * Tl::KV_BYTES, &v_full[st], ids[0]);
-      v_issued = j + 1;
-      return true;
-    };
-    for (int j = 0; j < NK; ++j) {
-      // in the order in which their stages come free
-      if constexpr (KSPLIT) {
-        if (!next_v(j) || !next_k(j)) break;
-      } else {
-        if (!next_k(j) || !next_v(j)) break;
+  if (producer) {
+    // ---------------- producers: the rest of their operand's tiles ----------------
+    int k_issued = ahead, v_issued = ahead;
+    for (int j = ahead; j < NK; ++j) {
+      if (one_warp || !is_v) {
+        if (!stage_free(false, j)) break;
+        load_tile(false, j, next_id);
+        k_issued = j + 1;
       }
-#pragma unroll
-      for (int a = 0; a < Tl::LEAD; ++a) ids[a] = ids[a + 1];
-      if (j + Tl::LEAD + 1 < NK) ids[Tl::LEAD] = block_id(j + Tl::LEAD + 1);
+      if (one_warp || is_v) {
+        if (!stage_free(true, j)) break;
+        load_tile(true, j, next_id);
+        v_issued = j + 1;
+      }
+      if (j + 1 < NK) next_id = block_id(j + 1);
     }
     // copies in flight land before the CTA can exit
     if (lane == 0) {
       mbar_wait_bounded(q_full, 0);
-      for (int kj = max(k_issued - Tl::KST, 0); kj < k_issued; ++kj)
-        mbar_wait_bounded(&k_full[kj % Tl::KST], (kj / Tl::KST) & 1);
-      for (int vj = max(v_issued - Tl::VST, 0); vj < v_issued; ++vj)
-        mbar_wait_bounded(&v_full[vj % Tl::VST], (vj / Tl::VST) & 1);
+      if (one_warp || !is_v)
+        for (int j = max(k_issued - Tl::KST, 0); j < k_issued; ++j)
+          mbar_wait_bounded(&k_full[j % Tl::KST], (j / Tl::KST) & 1);
+      if (one_warp || is_v)
+        for (int j = max(v_issued - Tl::VST, 0); j < v_issued; ++j)
+          mbar_wait_bounded(&v_full[j % Tl::VST], (j / Tl::VST) & 1);
     }
     __syncwarp();
   } else if (warp == kIssuer) {
-    // ---------------- MMA issuer (lane 0), V tail zeroing (whole warp) ----------------
+    // ---------------- MMA issuer (one elected lane), V tail zeroing (whole warp) ----------------
     constexpr int fmt = LO ? 1 : 0;
     constexpr uint32_t idesc_s = tc::instr_desc_f16(fmt, 0, 0, Tl::BM, BN);
     constexpr uint32_t idesc_o = tc::instr_desc_f16(fmt, 0, 1, Tl::BM, D);
-    const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
+    const uint32_t on = elect_one();
+    // (addresses are counted in 16 bytes in a descriptor's low 14 bits: a tile's
+    // step adds to them without a carry)
+    const uint64_t dQ = tc::smem_desc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dK = tc::smem_desc_sw128(smem_u32(sK), 16, 1024);
+    // V's tile: for each cache block its COLB column blocks of S rows one after
+    // the other. As an MN-major operand 64 columns lie S rows apart, and 8 keys
+    // 8 rows (one cache block, for S = 8); 16 keys are a whole cache block, or a
+    // part of one.
+    const uint64_t dV = tc::smem_desc_sw128(smem_u32(sV), S * 128, S == 8 ? 1024 * Tl::COLB : 1024);
+    const int lg = S <= 16 ? 0 : 31 - __clz(S >> 4);  // log2 of a block's 16-key steps
     auto issue_s = [&](int t, int j) {  // S_t = Q K_j^T
-      const uint32_t qb = aQ + (KSPLIT ? 0 : t) * Tl::Q_BYTES;
-      const uint32_t kb = aK + (j % Tl::KST) * Tl::KV_BYTES;
+      const uint64_t qd = dQ + (KSPLIT ? 0 : t) * (Tl::Q_BYTES >> 4);
+      const uint64_t kd = dK + (j % Tl::KST) * (Tl::KV_BYTES >> 4);
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
-        const uint32_t off = (s >> 2) * Tl::CB_BYTES + (s & 3) * 32;
-        tc::mma_ss(tmem + t * 256, tc::smem_desc_sw128(qb + off, 16, 1024),
-                   tc::smem_desc_sw128(kb + off, 16, 1024), idesc_s, s > 0);
+        const uint32_t off = ((s >> 2) * Tl::CB_BYTES + (s & 3) * 32) >> 4;
+        mma_ss_on(on, tmem + t * 256, qd + off, kd + off, idesc_s, s > 0);
       }
-      tc::commit(&s_full[t]);
+      commit_on(on, &s_full[t]);
     };
-    auto issue_pv = [&](int t, int st, bool accumulate) {  // O_t += P_t V
-      const uint32_t vb = aV + st * Tl::KV_BYTES;
+    auto issue_pv = [&](int t, int st, uint32_t accumulate) {  // O_t += P_t V
+      const uint64_t vd = dV + st * (Tl::KV_BYTES >> 4);
       const uint32_t tS = tmem + t * 256, tO = tS + 128;
 #pragma unroll
       for (int s = 0; s < BN / 16; ++s) {
-        const uint64_t bdesc = tc::smem_desc_sw128(vb + s * 16 * 128, Tl::CB_BYTES, 1024);
+        const uint64_t bdesc =
+            vd + static_cast<uint32_t>((((s >> lg) * Tl::COLB << lg) + (s & ((1 << lg) - 1))) * 128);
         const uint32_t pa = tS + 32 * (s >> 1) + 8 * (s & 1);  // keys 16s .. 16s + 15
-        tc::mma_ts(tO, pa, bdesc, idesc_o, accumulate || s > 0);
-        if constexpr (LO) tc::mma_ts(tO, pa + 16, bdesc, idesc_o, true);
+        mma_ts_on(on, tO, pa, bdesc, idesc_o, s > 0 ? 1u : accumulate);
+        if constexpr (LO) mma_ts_on(on, tO, pa + 16, bdesc, idesc_o, 1u);
       }
     };
     auto k_ready = [&](int j) {
@@ -344,15 +491,13 @@ __global__ void __launch_bounds__(576, 1)
     };
     bool ok = wait_warp(q_full, 0, abort_flag) && k_ready(0);
     if (ok) {
-      if (lane == 0) {
-        for (int t = 0; t < nq; ++t) issue_s(t, 0);
-        tc::commit(&k_empty[0]);
-      }
+      for (int t = 0; t < nq; ++t) issue_s(t, 0);
+      commit_on(on, &k_empty[0]);
       if (KSPLIT && NK > 1) {
         ok = k_ready(1);
-        if (ok && lane == 0) {
+        if (ok) {
           issue_s(1, 1);
-          tc::commit(&k_empty[1 % Tl::KST]);
+          commit_on(on, &k_empty[1 % Tl::KST]);
         }
       }
     }
@@ -364,12 +509,14 @@ __global__ void __launch_bounds__(576, 1)
       if (kb + BN > t_end) {
         // keys past the end: P is 0 there, and 0 * NaN would not be
         uint8_t* vs = sV + st * Tl::KV_BYTES;
-        for (int r = t_end - kb + lane; r < BN; r += 32)
+        for (int r = t_end - kb + lane; r < BN; r += 32) {
+          uint8_t* row = vs + (r / S * Tl::COLB * S + r % S) * 128;
 #pragma unroll
           for (int c = 0; c < Tl::COLB; ++c)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              reinterpret_cast<uint4*>(vs + c * Tl::CB_BYTES + r * 128)[k] = make_uint4(0, 0, 0, 0);
+              reinterpret_cast<uint4*>(row + c * S * 128)[k] = make_uint4(0, 0, 0, 0);
+        }
         tc::fence_proxy_async_smem();
         __syncwarp();
       }
@@ -378,45 +525,38 @@ __global__ void __launch_bounds__(576, 1)
         ok = wait_warp(&p_full[t], (j >> 1) & 1, abort_flag);
         if (!ok) break;
         tc::fence_after_sync();
-        if (lane == 0) {
-          issue_pv(t, st, j > 1);
-          if (j + 2 >= NK) tc::commit(&o_done[t]);
-          tc::commit(&v_empty[st]);
-        }
+        issue_pv(t, st, j > 1);
+        if (j + 2 >= NK) commit_on(on, &o_done[t]);
+        commit_on(on, &v_empty[st]);
         if (j + 2 < NK) {
           ok = k_ready(j + 2);
           if (!ok) break;
-          if (lane == 0) {
-            issue_s(t, j + 2);
-            tc::commit(&k_empty[(j + 2) % Tl::KST]);
-          }
+          issue_s(t, j + 2);
+          commit_on(on, &k_empty[(j + 2) % Tl::KST]);
         }
       } else {
         for (int t = 0; ok && t < nq; ++t) {
           ok = wait_warp(&p_full[t], j & 1, abort_flag);
           if (!ok) break;
           tc::fence_after_sync();
-          if (lane == 0) {
-            issue_pv(t, st, j > 0);
-            if (j == NK - 1) tc::commit(&o_done[t]);
-          }
+          issue_pv(t, st, j > 0);
+          if (j == NK - 1) commit_on(on, &o_done[t]);
           if (j + 1 < NK) {
             ok = k_ready(j + 1);
             if (!ok) break;
-            if (lane == 0) issue_s(t, j + 1);
+            issue_s(t, j + 1);
           }
         }
-        if (ok && lane == 0) {
-          tc::commit(&v_empty[st]);
-          if (j + 1 < NK) tc::commit(&k_empty[(j + 1) % Tl::KST]);
+        if (ok) {
+          commit_on(on, &v_empty[st]);
+          if (j + 1 < NK) commit_on(on, &k_empty[(j + 1) % Tl::KST]);
         }
       }
     }
     // every MMA issued has completed before tensor memory is released
-    if (lane == 0) {
-      tc::commit(mma_done);
-      mbar_wait_bounded(mma_done, 0);
-    }
+    __syncwarp();
+    commit_on(on, mma_done);
+    mbar_wait_bounded(mma_done, 0);
     __syncwarp();
   } else {
     // ---------------- softmax: warps 8t .. 8t + 7 serve stream t; warpgroup half
@@ -446,10 +586,10 @@ __global__ void __launch_bounds__(576, 1)
       ok = wait_warp(&s_full[t], j & 1, abort_flag);
       if (!ok) break;
       if (!warp_on) {  // (one arrival per phase: it waits for the phase it arrived at)
-        mbar_arrive(&xch_bar[t]);
+        arrive_warp(&xch_bar[t], lane);
         ok = wait_warp(&xch_bar[t], j & 1, abort_flag);
         if (!ok) break;
-        mbar_arrive(&p_full[t]);
+        arrive_warp(&p_full[t], lane);
         continue;
       }
       tc::fence_after_sync();
@@ -475,7 +615,7 @@ __global__ void __launch_bounds__(576, 1)
       // the row's max over both halves (slots alternate with the key tile, so a
       // half never overwrites a value the other has not read yet)
       slot(j, hw)[r] = hmax;
-      mbar_arrive(&xch_bar[t]);
+      arrive_warp(&xch_bar[t], lane);
       ok = wait_warp(&xch_bar[t], j & 1, abort_flag);
       if (!ok) break;
       const float tmax = fmaxf(hmax, slot(j, hw ^ 1)[r]) * p.scale_log2;
@@ -531,77 +671,87 @@ __global__ void __launch_bounds__(576, 1)
       l = l * alpha + ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y));
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(&p_full[t]);
+      arrive_warp(&p_full[t], lane);
     }
     // the row's sum over both halves
     if (ok) {
       slot(nkt, hw)[r] = l;
-      mbar_arrive(&xch_bar[t]);
+      arrive_warp(&xch_bar[t], lane);
       ok = wait_warp(&xch_bar[t], nkt & 1, abort_flag);
     }
     if (ok) l += slot(nkt, hw ^ 1)[r];
     if (ok) ok = wait_warp(&o_done[t], 0, abort_flag);
-    float w0 = 1.f, w1 = 0.f;  // weights of this stream's result and of the other's
-    float* jO = reinterpret_cast<float*>(sK);   // [D][128] stream 1's output, by column
-    float* jml = reinterpret_cast<float*>(sV);  // [2][128] its m and l
+    // The output columns this warp finishes, and its weights: of this stream's
+    // result and (KSPLIT) of the other's. Joining, stream t finishes the t-th half
+    // of each half's columns, and leaves the others to the other stream.
+    constexpr int FC = KSPLIT ? HD / 2 : HD;   // columns to finish
+    constexpr int CH = FC < 32 ? FC : 32;      // columns at a time
+    const int col0 = hw * HD + (KSPLIT ? t * FC : 0);
+    float w0 = 1.f, w1 = 0.f;
+    // 4 KB for its output on the way out: of the stream's query tile, or, of a
+    // single stream, of the K ring
+    uint8_t* buf = (NST == 1 ? sK : sQ + (KSPLIT ? 0 : t) * Tl::Q_BYTES) + (warp & 7) * 4096;
+    static_assert(NST == 1 ? Tl::KST * Tl::KV_BYTES >= 32768 : Tl::Q_BYTES >= 32768, "8 warps");
+    float* jO = reinterpret_cast<float*>(sK);   // [D][128] the columns left, by column
+    float* jml = reinterpret_cast<float*>(sV);  // [stream][2][128] m and l
+    bool join = false;
     if constexpr (KSPLIT) {
-      // Stream 1 leaves its result in the rings' memory once both streams' MMAs
-      // are done with them; stream 0 joins it to its own.
-      if (t == 1 && ok) ok = wait_warp(&o_done[0], 0, abort_flag);
-      if (t == 1 && ok && warp_on) {
+      if (t == 1) buf = sV + 32768 + (warp & 7) * 4096;
+      join = nk[1] > 0;
+      // The rings' memory is free once both streams' MMAs are done with it.
+      if (join && ok) ok = wait_warp(&o_done[t ^ 1], 0, abort_flag);
+      if (join && ok && warp_on) {
         tc::fence_after_sync();
+        const int left = hw * HD + (t ^ 1) * FC;  // columns for the other stream
 #pragma unroll 1
-        for (int c4 = 0; c4 < HD / 32; ++c4) {
-          uint32_t u[32];
-          tc::tmem_ld32(tO + c4 * 32, u);
+        for (int c0 = 0; c0 < FC; c0 += CH) {
+          uint32_t u[CH];
+          tmem_ld_cols(tT + 128 + left + c0, u);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            jO[(hw * HD + c4 * 32 + c) * 128 + r] = __uint_as_float(u[c]);
+          for (int c = 0; c < CH; ++c) jO[(left + c0 + c) * 128 + r] = __uint_as_float(u[c]);
         }
         if (hw == 0) {
-          jml[r] = m;
-          jml[128 + r] = l;
+          jml[t * 256 + r] = m;
+          jml[t * 256 + 128 + r] = l;
         }
       }
       asm volatile("bar.sync 1, 512;" ::: "memory");  // every softmax thread, aborted or not
-      if (t == 1) ok = false;
-      if (ok && nk[1] > 0) {
-        const float m1 = jml[r], l1 = jml[128 + r];
-        const float M = fmaxf(m, m1);
+      if (join && ok) {
+        const float mo = jml[(t ^ 1) * 256 + r], lo = jml[(t ^ 1) * 256 + 128 + r];
+        const float M = fmaxf(m, mo);
         w0 = m == -INFINITY ? 0.f : fast_exp2(m - M);
-        w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
-        l = w0 * l + w1 * l1;
+        w1 = mo == -INFINITY ? 0.f : fast_exp2(mo - M);
+        l = w0 * l + w1 * lo;
         m = M;
       }
+      // one key tile: stream 0 alone has a result, and finishes all its columns
     }
     if (ok && warp_on) {
       tc::fence_after_sync();
       const int64_t ih = static_cast<int64_t>(tok) * p.H + head;
       const float inv = direct ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
       const float f0 = w0 * inv, f1 = w1 * inv;
-      const bool join = KSPLIT && nk[NST - 1] > 0;
+      const int rows = nrow[t] - (warp & 3) * 32;  // this warp's
+      const int n_cols = KSPLIT && !join ? HD : FC;
+      void* dst = direct ? p.out : static_cast<void*>(p.ws_acc);
+      const pa_dtype dst_dt = direct ? p.out_dt : PA_F32;
+      const int64_t row_at = (direct ? ih : ih * p.NP + part) * D;
 #pragma unroll 1
-      for (int c4 = 0; c4 < HD / 32; ++c4) {
-        uint32_t u[32];
-        tc::tmem_ld32(tO + c4 * 32, u);
+      for (int c0 = 0; c0 < n_cols; c0 += CH) {
+        uint32_t u[CH];
+        tmem_ld_cols(tT + 128 + col0 + c0, u);
         tc::tmem_wait_ld();
-        float v[32];
+        float v[CH];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(u[c]) * f0;
+        for (int c = 0; c < CH; ++c) v[c] = __uint_as_float(u[c]) * f0;
         if (join) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            v[c] = fmaf(jO[(hw * HD + c4 * 32 + c) * 128 + r], f1, v[c]);
+          for (int c = 0; c < CH; ++c) v[c] = fmaf(jO[(col0 + c0 + c) * 128 + r], f1, v[c]);
         }
-        if (row_on) {
-          if (direct)
-            store_out32(p.out, p.out_dt, ih * D + hw * HD + c4 * 32, v);
-          else
-            store_row32<float>(p.ws_acc + (ih * p.NP + part) * D + hw * HD + c4 * 32, v);
-        }
+        store_out<CH>(buf, v, dst, dst_dt, row_at + col0 + c0, rows, lane);
       }
-      if (!direct && hw == 0 && row_on) {
+      if (!direct && hw == 0 && row_on && (!join || t == 0)) {
         p.ws_m[ih * p.NP + part] = m;
         p.ws_l[ih * p.NP + part] = l;
       }
