@@ -440,7 +440,7 @@ pa_status pa_cross(void* out, pa_dtype out_dt, const void* q, const void* k_cach
  * max_group requests are flagged PA_DEVERR_SEQ_LEN, with undefined output rows.
  * A request shorter than its group's shared part is exact as long as the V
  * values of the group's shared tokens are finite. D 64, 128 or 256; S 8, 16 or
- * 32; H / Hkv at most 128; B, NG <= 65535; NB * Hkv * S <= 2^31 - 1; scale finite
+ * 32; H / Hkv at most 128; B, NG <= 65534; NB * Hkv * S <= 2^31 - 1; scale finite
  * and > 0; 16-byte aligned q, out, caches and workspace.
  * ------------------------------------------------------------------------- */
 size_t pa_decode_shared_workspace_bytes(int B, int NG, int H, int Hkv, int D, int S, int max_group,

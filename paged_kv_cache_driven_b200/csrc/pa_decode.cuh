@@ -188,6 +188,12 @@ __global__ void __launch_bounds__(DecodeTiling<D, S, sizeof(TC), WIDE>::NW * 32)
   const int part = blockIdx.x;  // in a cluster launch, also the CTA's rank
   const int h = blockIdx.y;
   const int i = blockIdx.z;
+  if constexpr (std::is_same<Prm, DecodeParamsTail>::value) {
+    if (i == p.B) {  // the plane behind the requests: one CTA stays until the pass before is done
+      if (part == 0 && h == 0) grid_dependency_wait();
+      return;
+    }
+  }
   const int lane = threadIdx.x & 31;
   const int w = threadIdx.x >> 5;
   if constexpr (APPEND && EB == 1) {

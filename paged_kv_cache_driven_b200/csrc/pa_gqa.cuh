@@ -132,6 +132,22 @@ __device__ __forceinline__ float2 unpack2(uint32_t x) {
   return Elem<T>::pair(x);
 }
 
+// CTAs per SM asked of the compiler (0: its choice). Few rows at head size 64 in
+// two column tiles took 112 registers, four CTAs; with five (eight documents of
+// 992 to 4,000 shared tokens, 3 to 16 requests each) 76.2 -> 71.5 us, and no more with
+// six, which spill.
+template <typename Prm>
+constexpr int gqa_min_ctas(int D, int NHT) {
+  return std::is_same<Prm, DecodeParamsFew>::value && D == 64 && NHT == 2 ? 5 : 0;
+}
+
+// 2^x with the hardware approximation (relative error about 2^-22; 2^-inf = 0).
+__device__ __forceinline__ float approx_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // TC: the cache element type, T or E4M3 codes (per-tensor scales: K's folded
 // into q_scale, V's applied to the output). Over E4M3 the consumers convert
 // each staged unit to f16 tiles and the products run in f16 (E4M3 values are
@@ -148,7 +164,8 @@ __device__ __forceinline__ float2 unpack2(uint32_t x) {
 // part among the CTA's requests, a column sees those of its own request.
 template <typename T, typename TO, int D, int S, bool APPEND, int NHT, typename TC = T,
           typename Prm = DecodeParams>
-__global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
+__global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
+                                  gqa_min_ctas<Prm>(D, NHT))
     paged_decode_gqa_kernel(const Prm p, const __grid_constant__ CUtensorMap tmk,
                             const __grid_constant__ CUtensorMap tmv) {
   constexpr int EB = sizeof(TC);
@@ -166,6 +183,12 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
   const int part = blockIdx.x;
   const int G = p.H / p.Hkv;
   const int i = blockIdx.z;
+  if constexpr (std::is_same<Prm, DecodeParamsTail>::value) {
+    if (i == p.B) {  // the plane behind the requests: one CTA stays until the pass before is done
+      if (part == 0 && blockIdx.y == 0) grid_dependency_wait();
+      return;
+    }
+  }
   int rows = G;        // query rows of this KV head
   int q0 = 0;          // FEW: the item's first query token
   int most_rows = G;   // rows that the grid has CTAs for
@@ -205,6 +228,7 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
   const int32_t* trow = p.block_tables + static_cast<int64_t>(i) * p.MB;
   int width = p.MB;  // entries of the table row from trow on
   constexpr bool TAIL = std::is_same<Prm, DecodeParamsTail>::value;
+  constexpr bool FAST = FEW || TAIL;
   int L = 0;
   bool grouped = false;  // FEW: the shared part of a group of requests
   if constexpr (FEW) grouped = p.shared_lens != nullptr;
@@ -636,10 +660,18 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32)
         for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, off));
         const float mn = fmaxf(m[nt][c], mx);
         // a unit with no valid token for this head keeps its max at -inf
-        al[nt][c] = mn == -INFINITY ? 1.f : exp2f(m[nt][c] - mn);
-        any_rescale |= al[nt][c] != 1.f;
-        pr[c] = sc[c] == -INFINITY ? 0.f : exp2f(sc[c] - mn);
-        pr[c + 2] = sc[c + 2] == -INFINITY ? 0.f : exp2f(sc[c + 2] - mn);
+        if constexpr (FAST) {  // (2^-inf is 0: only a column without keys so far needs care)
+          const float mr = mn == -INFINITY ? 0.f : mn;
+          al[nt][c] = approx_exp2(m[nt][c] - mr);
+          any_rescale |= m[nt][c] < mn;
+          pr[c] = approx_exp2(sc[c] - mr);
+          pr[c + 2] = approx_exp2(sc[c + 2] - mr);
+        } else {
+          al[nt][c] = mn == -INFINITY ? 1.f : exp2f(m[nt][c] - mn);
+          any_rescale |= al[nt][c] != 1.f;
+          pr[c] = sc[c] == -INFINITY ? 0.f : exp2f(sc[c] - mn);
+          pr[c + 2] = sc[c + 2] == -INFINITY ? 0.f : exp2f(sc[c + 2] - mn);
+        }
         l[nt][c] = l[nt][c] * al[nt][c] + pr[c] + pr[c + 2];
         m[nt][c] = mn;
       }

@@ -33,15 +33,46 @@ __global__ void __launch_bounds__(128)
 namespace host {
 namespace {
 
+// The tails' launch. Right behind the shared part's pass it is a programmatic
+// dependent of it, which lets its CTAs take the SMs that the last wave of that
+// pass leaves idle: both only read the inputs and write slots of their own. The
+// merge, the next dependent, needs both passes; so the grid has a plane more,
+// one CTA of which waits for the shared part's pass to be done (blockIdx.z == B).
+template <typename Kern, typename... Args>
+pa_status launch_tail_pass(Kern kern, dim3 grid, int threads, int smem, bool overlap,
+                           cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = overlap ? dim3(grid.x, grid.y, grid.z + 1) : grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? cuda_status() : PA_ERR_CUDA;
+}
+
 // One KV head per query head: one CTA per (partition, head, request).
-template <typename T, int D, int S>
+template <typename T, int D, int S, bool WIDE>
 pa_status tails_single(const DecodeParamsTail& prm, cudaStream_t stream) {
-  using Tl = DecodeTiling<D, S, 2, true>;
-  auto kern = paged_decode_partition_kernel<T, float, D, S, false, T, false, DecodeParamsTail, true>;
+  using Tl = DecodeTiling<D, S, 2, WIDE>;
+  auto kern = paged_decode_partition_kernel<T, float, D, S, false, T, false, DecodeParamsTail, WIDE>;
   static bool configured[kMaxDevices] = {};
   if (!opt_in_smem(kern, Tl::SMEM, configured)) return PA_ERR_CUDA;
-  kern<<<dim3(prm.tail_parts, prm.H, prm.B), Tl::NW * 32, Tl::SMEM, stream>>>(prm);
-  return cuda_status();
+  return launch_tail_pass(kern, dim3(prm.tail_parts, prm.H, prm.B), Tl::NW * 32, Tl::SMEM,
+                          prm.part0 > 0, stream, prm);
+}
+
+// (wide CTAs for up to four of them per SM, as pa_decode's)
+template <typename T, int D, int S>
+pa_status tails_single(const DecodeParamsTail& prm, cudaStream_t stream) {
+  constexpr bool two = DecodeTiling<D, S, 2, false>::NW != DecodeTiling<D, S, 2, true>::NW;
+  const int64_t ctas = static_cast<int64_t>(prm.tail_parts) * prm.H * prm.B;
+  if (two && ctas <= 4 * static_cast<int64_t>(sm_count()))
+    return tails_single<T, D, S, two>(prm, stream);
+  return tails_single<T, D, S, false>(prm, stream);
 }
 
 // Grouped heads: one CTA per (partition, KV head and chunk of 16 heads, request).
@@ -59,8 +90,8 @@ pa_status tails_grouped(const DecodeParamsTail& prm, cudaStream_t stream) {
     return PA_ERR_CUDA;
   const int G = prm.H / prm.Hkv;
   const dim3 grid(prm.tail_parts, prm.Hkv * ((G + 15) / 16), prm.B);
-  kern<<<grid, (Tg::NC + 1) * 32, Tg::SMEM, stream>>>(prm, tmk, tmv);
-  return cuda_status();
+  return launch_tail_pass(kern, grid, (Tg::NC + 1) * 32, Tg::SMEM, prm.part0 > 0, stream, prm, tmk,
+                          tmv);
 }
 
 template <typename T>
