@@ -470,12 +470,6 @@ def _all_contiguous(names, tensors):
             raise ValueError(f"{names[n]} must be contiguous")
 
 
-def _of_type(names, tensors, dtype):
-    for n, t in enumerate(tensors):
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"{names[n]} must be {dtype}".replace("torch.", ""))
-
-
 def _half_type(t, name):
     dt = t.dtype
     if dt != torch.bfloat16 and dt != torch.float16:
@@ -483,32 +477,41 @@ def _half_type(t, name):
     return dt
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
+def _rows(t, name, T, D, dt):
+    """(address, elements from one token to the next, heads) of t [T, heads, D]: tokens may be
+    strided, the heads of a token are contiguous."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype != dt or len(shape) != 3 or shape[0] != T or shape[2] != D:
+        raise ValueError(f"{name} must be {dt} [{T}, heads, {D}]".replace("torch.", ""))
+    heads = shape[1]
+    if stride[2] != 1 or (stride[1] != D and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), stride[0] if T > 1 else heads * D, heads  # (one token has no next one)
 
 
-def _launch(name, idx, stream, *args):
-    """The entry point `name` on device `idx`: on `stream`, or that device's current stream."""
-    fn = getattr(lib(), name)
-    raw = torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream
+def _vector(t, name, n, dt):
+    """The address of a contiguous vector of n elements (None: not given)."""
+    if t is None:
+        return None
+    if t.dtype != dt or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dt} [{n}]".replace("torch.", ""))
+    return t.data_ptr()
+
+
+def _raw_stream(idx, stream):
+    return torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream
+
+
+def _launch(name, idx, *args):
+    """The entry point `name` with device `idx` current."""
+    fn = getattr(_lib or lib(), name)
     if torch._C._cuda_getDevice() == idx:
-        rc = fn(*args, raw)
+        rc = fn(*args)
     else:
         with torch.cuda.device(idx):
-            rc = fn(*args, raw)
+            rc = fn(*args)
     if rc != PA_OK:
         raise PagedAttnError(rc, name)
-
-
-def _token_stride(t, name):
-    """Elements from one token's rows to the next's of t [T, heads, D], heads contiguous."""
-    T, heads, D = t.shape
-    if T == 0 or heads == 0:
-        return heads * D
-    step, head, one = t.stride()
-    if one != 1 or (head != D and heads > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return step if T > 1 else heads * D  # (one token has no next one)
 
 
 def pa_rope_table(rot_dim, base=10000.0, scaling=PA_ROPE_PLAIN, factor=1.0, low=1.0, high=32.0,
@@ -524,31 +527,9 @@ def pa_rope_table(rot_dim, base=10000.0, scaling=PA_ROPE_PLAIN, factor=1.0, low=
     return table, amplitude.value
 
 
-_ROPE_NAMES = ("positions", "table", "q_weight", "k_weight", "q", "k", "q_out", "k_out")
-_APPEND_NAMES = ("positions", "table", "q_weight", "k_weight", "slot_mapping", "k_cache",
-                 "v_cache", "q", "k", "q_out", "v")
-
-
-def _rope_common(q, k, q_out, positions, table, q_weight, k_weight):
-    """Checks shared by the pa_rope calls; returns (dtype, T, H, Hkv, D)."""
-    dt = _half_type(q, "q")
-    _of_type(("k", "q_out", "q_weight", "k_weight"), (k, q_out, q_weight, k_weight), dt)
-    if positions.dtype != torch.int32:
-        raise ValueError("positions must be int32")
-    if table.dtype != torch.float64:
-        raise ValueError("table must be float64")
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q must be [T, H, D] and k [T, Hkv, D]")
-    T, H, D = q.shape
-    Tk, Hkv, Dk = k.shape
-    if Tk != T or Dk != D or q_out.shape != q.shape:
-        raise ValueError("q and q_out must be [T, H, D] and k [T, Hkv, D]")
-    if positions.shape != (T,) or table.dim() != 1:
-        raise ValueError("positions must be [T] and table [rot_dim / 2]")
-    if (q_weight is not None and q_weight.shape != (D,)) or \
-            (k_weight is not None and k_weight.shape != (D,)):
-        raise ValueError("q_weight and k_weight must be [D]")
-    return dt, T, H, Hkv, D
+_ROPE_NAMES = ("q", "k", "q_out", "k_out", "positions", "table", "q_weight", "k_weight")
+_APPEND_NAMES = ("q", "k", "v", "q_out", "positions", "slot_mapping", "k_cache", "v_cache", "table",
+                 "q_weight", "k_weight")
 
 
 def pa_rope(q_out, k_out, q, k, positions, table, interleaved=False, amplitude=1.0, q_weight=None,
@@ -556,44 +537,51 @@ def pa_rope(q_out, k_out, q, k, positions, table, interleaved=False, amplitude=1
     """Norms (where a weight [D] is given) and rotates q [T, H, D] and k [T, Hkv, D] at
     positions [T] (int32) into q_out, k_out (which may be q, k). Tokens may be strided, heads are
     contiguous; table: float64 [rot_dim / 2] on the device (pa_rope_table)."""
-    tensors = (positions, table, q_weight, k_weight, q, k, q_out, k_out)
-    idx = _one_device(_ROPE_NAMES, tensors)
-    _all_contiguous(_ROPE_NAMES, tensors[:4])
-    dt, T, H, Hkv, D = _rope_common(q, k, q_out, positions, table, q_weight, k_weight)
-    if k_out.dtype != dt or k_out.shape != k.shape:
-        raise ValueError("k_out must have k's type and shape")
-    _launch("pa_rope", idx, stream, q_out.data_ptr(), _token_stride(q_out, "q_out"),
-            k_out.data_ptr(), _token_stride(k_out, "k_out"), q.data_ptr(), _token_stride(q, "q"),
-            k.data_ptr(), _token_stride(k, "k"), positions.data_ptr(), table.data_ptr(),
-            2 * table.numel(), 1 if interleaved else 0, amplitude, _address(q_weight),
-            _address(k_weight), eps, T, H, Hkv, D, _DT[dt])
+    idx = _one_device(_ROPE_NAMES, (q, k, q_out, k_out, positions, table, q_weight, k_weight))
+    dt = _half_type(q, "q")
+    T, D = q.shape[0], q.shape[-1]
+    qp, qs, H = _rows(q, "q", T, D, dt)
+    kp, ks, Hkv = _rows(k, "k", T, D, dt)
+    qop, qos, qoh = _rows(q_out, "q_out", T, D, dt)
+    kop, kos, koh = _rows(k_out, "k_out", T, D, dt)
+    if qoh != H or koh != Hkv:
+        raise ValueError("q_out and k_out must have the heads of q and k")
+    half = table.numel()
+    _launch("pa_rope", idx, qop, qos, kop, kos, qp, qs, kp, ks,
+            _vector(positions, "positions", T, torch.int32),
+            _vector(table, "table", half, torch.float64), 2 * half, 1 if interleaved else 0,
+            amplitude, _vector(q_weight, "q_weight", D, dt), _vector(k_weight, "k_weight", D, dt),
+            eps, T, H, Hkv, D, _DT[dt], _raw_stream(idx, stream))
 
 
 def _rope_append(name, q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, scales, table,
                  interleaved, amplitude, q_weight, k_weight, eps, stream):
-    tensors = (positions, table, q_weight, k_weight, slot_mapping, k_cache, v_cache, q, k, q_out, v)
-    idx = _one_device(_APPEND_NAMES, tensors)
-    _all_contiguous(_APPEND_NAMES, tensors[:7])
-    dt, T, H, Hkv, D = _rope_common(q, k, q_out, positions, table, q_weight, k_weight)
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
-        raise ValueError("slot_mapping must be int64 [T]")
-    if v.dtype != dt or v.shape != k.shape:
-        raise ValueError("v must have k's type and shape")
+    idx = _one_device(_APPEND_NAMES, (q, k, v, q_out, positions, slot_mapping, k_cache, v_cache,
+                                      table, q_weight, k_weight))
+    dt = _half_type(q, "q")
+    T, D = q.shape[0], q.shape[-1]
+    qp, qs, H = _rows(q, "q", T, D, dt)
+    kp, ks, Hkv = _rows(k, "k", T, D, dt)
+    vp, vs, vh = _rows(v, "v", T, D, dt)
+    qop, qos, qoh = _rows(q_out, "q_out", T, D, dt)
+    if qoh != H or vh != Hkv:
+        raise ValueError("q_out must have the heads of q, v those of k")
     cdt = torch.uint8 if scales else dt
     if k_cache.dtype != cdt or v_cache.dtype != cdt:
         raise ValueError("E4M3 caches are uint8 tensors of codes" if scales
                          else "q, k, v and the caches must share one dtype")
-    if k_cache.dim() != 4:
-        raise ValueError("the caches must be [NB, Hkv, S, D]")
-    NB, Hc, S, Dc = k_cache.shape
-    if Hc != Hkv or Dc != D or v_cache.shape != k_cache.shape:
-        raise ValueError("the caches must be [NB, Hkv, S, D]")
-    _launch(name, idx, stream, q_out.data_ptr(), _token_stride(q_out, "q_out"), q.data_ptr(),
-            _token_stride(q, "q"), k.data_ptr(), _token_stride(k, "k"), v.data_ptr(),
-            _token_stride(v, "v"), positions.data_ptr(), slot_mapping.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), *scales, table.data_ptr(), 2 * table.numel(),
-            1 if interleaved else 0, amplitude, _address(q_weight), _address(k_weight), eps, T, H,
-            Hkv, D, S, NB, _DT[dt])
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1] != Hkv or shape[3] != D or v_cache.shape != shape or \
+            not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise ValueError("the caches must be contiguous [NB, Hkv, S, D]")
+    half = table.numel()
+    _launch(name, idx, qop, qos, qp, qs, kp, ks, vp, vs,
+            _vector(positions, "positions", T, torch.int32),
+            _vector(slot_mapping, "slot_mapping", T, torch.int64), k_cache.data_ptr(),
+            v_cache.data_ptr(), *scales, _vector(table, "table", half, torch.float64), 2 * half,
+            1 if interleaved else 0, amplitude, _vector(q_weight, "q_weight", D, dt),
+            _vector(k_weight, "k_weight", D, dt), eps, T, H, Hkv, D, shape[2], shape[0], _DT[dt],
+            _raw_stream(idx, stream))
 
 
 def pa_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, table,
@@ -623,25 +611,28 @@ _SHARED_NAMES = ("out", "q", "k_cache", "v_cache", "block_tables", "workspace", 
 
 def _paged_common(names, tensors):
     """Checks shared by pa_cross and pa_decode_shared (tensors in the order of their names);
-    returns (device index, workspace bytes)."""
+    returns (device index, shapes of q and k_cache, their type, workspace address and bytes)."""
     idx = _one_device(names, tensors)
     _all_contiguous(names, tensors)
     out, q, k_cache, v_cache, block_tables, workspace = tensors[:6]
     dt = _half_type(q, "q")
     if k_cache.dtype != dt or v_cache.dtype != dt:
         raise ValueError("q and the caches must share one dtype")
-    if block_tables.dtype != torch.int32:
-        raise ValueError("block_tables must be int32")
-    _of_type(names[6:], tensors[6:], torch.int32)
+    for n in range(4, len(tensors)):
+        if n != 5 and tensors[n].dtype != torch.int32:
+            raise ValueError(f"{names[n]} must be int32")
     if out.dtype not in _DT:
         raise ValueError("out must be float32, float16 or bfloat16")
-    if q.dim() != 3 or out.shape != q.shape:
+    qs, cs = q.shape, k_cache.shape
+    if len(qs) != 3 or out.shape != qs:
         raise ValueError("q and out must be [rows, H, D]")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != q.shape[2]:
+    if len(cs) != 4 or v_cache.shape != cs or cs[3] != qs[2]:
         raise ValueError("the caches must be [NB, Hkv, S, D]")
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be [B, MB]")
-    return idx, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if workspace is None:
+        return idx, qs, cs, dt, None, 0
+    return idx, qs, cs, dt, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def pa_cross_workspace_bytes(B, T, H, Hkv, D, max_q_len, max_kv_len, partition=0):
@@ -653,17 +644,16 @@ def pa_cross(out, q, k_cache, v_cache, block_tables, kv_lens, q_start, scale, ma
     """Cross attention over cached states: rows q_start[i] .. q_start[i + 1] - 1 of q [T, H, D]
     each see all kv_lens[i] tokens of block_tables[i]; caches [NB, Hkv, S, D]. workspace: a
     CUDA uint8 tensor of pa_cross_workspace_bytes(...) bytes, or None when that is 0."""
-    idx, ws_bytes = _paged_common(_CROSS_NAMES, (out, q, k_cache, v_cache, block_tables, workspace,
-                                                 kv_lens, q_start))
-    T, H, D = q.shape
-    NB, Hkv, S, _ = k_cache.shape
+    idx, (T, H, D), (NB, Hkv, S, _), dt, ws, ws_bytes = _paged_common(
+        _CROSS_NAMES, (out, q, k_cache, v_cache, block_tables, workspace, kv_lens, q_start))
     B, MB = block_tables.shape
-    if kv_lens.shape != (B,) or q_start.shape != (B + 1,):
+    if kv_lens.dim() != 1 or kv_lens.numel() != B or q_start.dim() != 1 or \
+            q_start.numel() != B + 1:
         raise ValueError("kv_lens must be [B] and q_start [B + 1]")
-    _launch("pa_cross", idx, stream, out.data_ptr(), _DT[out.dtype], q.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), MB,
-            kv_lens.data_ptr(), q_start.data_ptr(), scale, B, H, Hkv, D, S, NB, _DT[q.dtype], T,
-            max_q_len, max_kv_len, partition, _address(workspace), ws_bytes)
+    _launch("pa_cross", idx, out.data_ptr(), _DT[out.dtype], q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), block_tables.data_ptr(), MB, kv_lens.data_ptr(),
+            q_start.data_ptr(), scale, B, H, Hkv, D, S, NB, _DT[dt], T, max_q_len, max_kv_len,
+            partition, ws, ws_bytes, _raw_stream(idx, stream))
 
 
 def pa_decode_shared_workspace_bytes(B, NG, H, Hkv, D, S, max_group, max_shared_len,
@@ -677,19 +667,19 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, seq_lens, shared_le
     """pa_decode_gqa's result for q, out [B, H, D] and caches [NB, Hkv, S, D], the first
     shared_lens[b] tokens of the requests of a group (group_start [NG + 1]) read once for the
     group. workspace: a CUDA uint8 tensor of pa_decode_shared_workspace_bytes(...) bytes."""
-    idx, ws_bytes = _paged_common(_SHARED_NAMES, (out, q, k_cache, v_cache, block_tables, workspace,
-                                                  seq_lens, shared_lens, group_start))
-    B, H, D = q.shape
-    NB, Hkv, S, _ = k_cache.shape
-    if block_tables.shape[0] != B or seq_lens.shape != (B,) or shared_lens.shape != (B,) \
-            or group_start.dim() != 1 or group_start.shape[0] < 1:
+    idx, (B, H, D), (NB, Hkv, S, _), dt, ws, ws_bytes = _paged_common(
+        _SHARED_NAMES, (out, q, k_cache, v_cache, block_tables, workspace, seq_lens, shared_lens,
+                        group_start))
+    rows, MB = block_tables.shape
+    if rows != B or seq_lens.dim() != 1 or seq_lens.numel() != B or shared_lens.dim() != 1 or \
+            shared_lens.numel() != B or group_start.dim() != 1 or group_start.numel() < 1:
         raise ValueError("block_tables must be [B, MB], seq_lens and shared_lens [B], "
                          "group_start [NG + 1]")
-    _launch("pa_decode_shared", idx, stream, out.data_ptr(), _DT[out.dtype], q.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], seq_lens.data_ptr(), shared_lens.data_ptr(),
-            group_start.data_ptr(), group_start.shape[0] - 1, scale, B, H, Hkv, D, S, NB,
-            _DT[q.dtype], max_group, max_shared_len, max_tail_len, _address(workspace), ws_bytes)
+    _launch("pa_decode_shared", idx, out.data_ptr(), _DT[out.dtype], q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), MB,
+            seq_lens.data_ptr(), shared_lens.data_ptr(), group_start.data_ptr(),
+            group_start.numel() - 1, scale, B, H, Hkv, D, S, NB, _DT[dt], max_group,
+            max_shared_len, max_tail_len, ws, ws_bytes, _raw_stream(idx, stream))
 
 
 def pa_copy_blocks(k_cache, v_cache, src_dst, stream=None):
