@@ -10,7 +10,7 @@ namespace pa {
 namespace host {
 namespace {
 
-template <typename T, int LAYOUT, int MODE, int LPR>
+template <typename T, int LAYOUT, int MODE, int EPT, int LPR>
 pa_status launch(RopeParams prm, cudaStream_t stream) {
   // Tokens that fill the GPU go kRopeTokens (as many as leave four CTAs per SM,
   // about 1,000 threads' rows each) to a CTA. Fewer tokens than two CTAs per
@@ -28,27 +28,29 @@ pa_status launch(RopeParams prm, cudaStream_t stream) {
     while (prm.toks < kRopeTokens && prm.toks * prm.rows < 16 * RPP &&
            static_cast<int64_t>(prm.T) >= 2 * prm.toks * 4 * sms)
       prm.toks *= 2;
-  // (rows < 16 RPP where toks > 1, so the numbers stay far below 2^16 and the
-  // multiplication divides exactly)
-  prm.row_magic = ((uint64_t{1} << 32) + prm.rows - 1) / prm.rows;
   const int64_t groups = ceil_div(prm.T, prm.toks);
-  rope_kernel<T, LAYOUT, MODE, LPR>
+  rope_kernel<T, LAYOUT, MODE, EPT, LPR>
       <<<static_cast<unsigned>(groups * chunks), 256, 0, stream>>>(prm);
   return cuda_status();
 }
 
-template <typename T, int LAYOUT, int MODE>
+template <typename T, int LAYOUT, int MODE, int EPT>
 pa_status by_size(const RopeParams& prm, cudaStream_t st) {
-  if (prm.D <= 64) return launch<T, LAYOUT, MODE, 8>(prm, st);
-  if (prm.D <= 128) return launch<T, LAYOUT, MODE, 16>(prm, st);
-  return launch<T, LAYOUT, MODE, 32>(prm, st);
+  if (prm.D <= 64) return launch<T, LAYOUT, MODE, EPT, 64 / EPT>(prm, st);
+  if (prm.D <= 128) return launch<T, LAYOUT, MODE, EPT, 128 / EPT>(prm, st);
+  return launch<T, LAYOUT, MODE, EPT, 256 / EPT>(prm, st);
 }
 
+// 16 elements per thread where head and rotation are multiples of 16 (in the
+// half layout each piece is then 8 aligned elements on one side of the
+// rotation's end), else 8, in the half layout one by one.
 template <typename T, int MODE>
 pa_status by_layout(const RopeParams& prm, int interleaved, cudaStream_t st) {
-  if (interleaved) return by_size<T, kPairs, MODE>(prm, st);
-  return prm.rot % 8 == 0 ? by_size<T, kHalf, MODE>(prm, st)
-                          : by_size<T, kHalfAny, MODE>(prm, st);
+  if (interleaved)
+    return prm.D % 16 == 0 ? by_size<T, kPairs, MODE, 16>(prm, st)
+                           : by_size<T, kPairs, MODE, 8>(prm, st);
+  return prm.D % 16 == 0 && prm.rot % 16 == 0 ? by_size<T, kHalf, MODE, 16>(prm, st)
+                                              : by_size<T, kHalfAny, MODE, 8>(prm, st);
 }
 
 template <typename T>

@@ -77,7 +77,6 @@ struct RopeParams {
   int chunks;                 // CTAs per token (1 where toks > 1)
   int chunk_rows;             // rows per CTA and token
   int toks;                   // tokens per CTA
-  uint64_t row_magic;         // ceil(2^32 / rows): n / rows = (n * row_magic) >> 32
 };
 
 // Attention of packed query rows over whole paged key ranges (pa_cross, and the
