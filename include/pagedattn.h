@@ -399,10 +399,12 @@ pa_status pa_rope_append_fp8(void* q_out, int64_t q_out_stride, const void* q, i
  *                 of this many tokens (a multiple of 128)
  *   workspace     as in pa_decode, pa_cross_workspace_bytes(...) for the same
  *                 arguments
- * D 64, 128 or 256; S one of 8, 16, 32, 64, 128; H / Hkv at most 128;
- * NB * Hkv * S <= 2^31 - 1; B <= 65535; scale finite and > 0. Errors as in pa_prefill
- * (a request whose q_start is inconsistent is skipped and flagged; kv_lens below
- * 0 count as 0 and are flagged).
+ * D 64, 128 or 256; S one of 8, 16, 32, 64, 128; H at most 65535, H / Hkv at
+ * most 128; NB * Hkv * S <= 2^31 - 1; B <= 65535; max_kv_len <= 2^31 - 128; scale
+ * finite and > 0. Errors as in pa_prefill (a request whose q_start is
+ * inconsistent is skipped and flagged; kv_lens below 0 count as 0 and are
+ * flagged). Both size functions below depend on the current device's SM count,
+ * as pa_decode_plan: call them with the device current that the call will run on.
  * ------------------------------------------------------------------------- */
 size_t pa_cross_workspace_bytes(int B, int T, int H, int Hkv, int D, int max_q_len, int max_kv_len,
                                 int partition);
@@ -440,7 +442,7 @@ pa_status pa_cross(void* out, pa_dtype out_dt, const void* q, const void* k_cach
  * max_group requests are flagged PA_DEVERR_SEQ_LEN, with undefined output rows.
  * A request shorter than its group's shared part is exact as long as the V
  * values of the group's shared tokens are finite. D 64, 128 or 256; S 8, 16 or
- * 32; H / Hkv at most 128; B, NG <= 65534; NB * Hkv * S <= 2^31 - 1; scale finite
+ * 32; H at most 65535, H / Hkv at most 128; B, NG <= 65534; NB * Hkv * S <= 2^31 - 1; scale finite
  * and > 0; 16-byte aligned q, out, caches and workspace.
  * ------------------------------------------------------------------------- */
 size_t pa_decode_shared_workspace_bytes(int B, int NG, int H, int Hkv, int D, int S, int max_group,

@@ -1038,7 +1038,8 @@ RowsPlan plan_rows(int items, int max_rows, int G, int Hkv, int D, int max_len, 
 bool rows_len_ok(int max_len) { return max_len >= 0 && max_len <= INT_MAX - (kKeyTile - 1); }
 
 bool rows_shape_ok(int H, int Hkv, int D) {
-  return H > 0 && Hkv > 0 && H % Hkv == 0 && H / Hkv <= 128 && (D == 64 || D == 128 || D == 256);
+  return H > 0 && Hkv > 0 && H % Hkv == 0 && H / Hkv <= 128 && H <= 65535 &&
+         (D == 64 || D == 128 || D == 256);
 }
 
 // Launches the attention over whole key ranges that `pl` chose.
@@ -1094,7 +1095,7 @@ SharedPlan plan_shared(int B, int NG, int H, int Hkv, int D, int S, int max_grou
 bool shared_bounds_ok(int B, int NG, int H, int Hkv, int D, int S, int max_group,
                       int max_shared_len, int max_tail_len) {
   // (the tails' grid has a plane more than requests)
-  return B >= 0 && NG >= 0 && B <= 65534 && NG <= 65534 && H <= 65535 && rows_shape_ok(H, Hkv, D) &&
+  return B >= 0 && NG >= 0 && B <= 65534 && NG <= 65534 && rows_shape_ok(H, Hkv, D) &&
          decode_shape_ok(D, S) && max_group >= 0 && rows_len_ok(max_shared_len) &&
          max_tail_len >= 0 && max_tail_len <= INT_MAX - 4096;
 }

@@ -783,7 +783,9 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
       for (int c = 0; c < NC; ++c) a = fmaf(wt[c], mg[(c * ROWS + row) * (D + 2) + 2 + d], a);
       if constexpr (EB == 1) a *= p.v_scale;
       if (direct) {
-        static_cast<TO*>(p.out)[ih * D + d] = to_out<TO>(lsum > 0.f ? a / lsum : 0.f);
+        // (FEW: a NaN in q or in a key stays NaN)
+        const bool some = FEW ? lsum != 0.f : lsum > 0.f;
+        static_cast<TO*>(p.out)[ih * D + d] = to_out<TO>(some ? a / lsum : 0.f);
       } else {
         p.ws_acc[wslot * D + d] = a;
       }

@@ -121,7 +121,9 @@ pa_status merge(const DecodeParamsTail& prm, int P_shared, pa_dtype out_dt, int 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  // (nothing was launched before it where no request can have a key: what runs
+  // before is then not ours, and it reads the lengths only after that)
+  cfg.numAttrs = prm.NP > 0 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D>, prm, P_shared, out_dt, S) == cudaSuccess
              ? cuda_status()
              : PA_ERR_CUDA;

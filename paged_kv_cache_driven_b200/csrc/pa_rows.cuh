@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
     if (ok && warp_on) {
       tc::fence_after_sync();
       const int64_t ih = static_cast<int64_t>(tok) * p.H + head;
-      const float inv = direct ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      const float inv = direct ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
       const float f0 = w0 * inv, f1 = w1 * inv;
       const int rows = nrow[t] - (warp & 3) * 32;  // this warp's
       const int n_cols = KSPLIT && !join ? HD : FC;
@@ -811,11 +811,12 @@ __device__ __forceinline__ void merge_row(const float* ws_m, const float* ws_l,
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) lsum += __shfl_xor_sync(kFullMask, lsum, o);
-  const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+  // (a sum that is NaN, of a NaN in q or in a key, stays NaN)
+  const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
   const int64_t at = ih * D + lane * DL;
 #pragma unroll
   for (int e = 0; e < DL; ++e) {
-    const float o = lsum > 0.f ? a[e] * inv : 0.f;
+    const float o = a[e] * inv;
     if (out_dt == PA_F32)
       static_cast<float*>(out)[at + e] = o;
     else if (out_dt == PA_BF16)

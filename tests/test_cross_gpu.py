@@ -153,6 +153,26 @@ def test_bad_inputs_are_flagged():
     assert torch.equal(out[:4], good[:4]) and bool((out[4:] == 7).all())
 
 
+@pytest.mark.parametrize("q_len,partition", [(1, -1), (1, 128), (3, 0), (40, -1), (300, -1),
+                                             (40, 128)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_stays_nan_where_it_belongs(D, q_len, partition):
+    """A NaN in a key of a request, or in one query row, makes NaN of the rows that see it and of no
+    others (zeros would hide it)."""
+    q_lens, kv_lens = [q_len, q_len], [600, 500]
+    c, q, qs = case(q_lens, kv_lens, 2, 2, D, 16, torch.bfloat16, seed=3)
+    good = call(c, q, qs, q_lens, kv_lens, partition=partition)
+    c.k_cache[c.tables_host[0][20], 1, 3, 5] = float("nan")  # token 323 of request 0, head 1
+    bad_row = 2 * q_len - 1
+    q[bad_row, 0, 7] = float("nan")
+    out = call(c, q, qs, q_lens, kv_lens, partition=partition)
+    want = torch.zeros(2 * q_len, 2, dtype=torch.bool, device=DEV)
+    want[:q_len, 1] = True
+    want[bad_row, 0] = True
+    assert torch.equal(out.isnan().all(-1), want) and torch.equal(out.isnan().any(-1), want)
+    assert torch.equal(out[~want], good[~want])
+
+
 def test_captured_on_two_streams():
     """Two captured calls with workspaces of their own, replayed at the same time."""
     q_lens, kv_lens = [1] * 3, [900, 1500, 64]

@@ -147,7 +147,7 @@ CROSS = dict(out=P, out_dt=binding.PA_F32, q=P, k=P, v=P, bt=P, MB=8, lens=P, st
 @pytest.mark.parametrize("bad", [
     dict(D=96), dict(D=32), dict(S=4), dict(S=24), dict(S=256), dict(dt=binding.PA_F32),
     dict(out_dt=7), dict(H=0), dict(Hkv=0), dict(H=9), dict(H=1032, Hkv=8), dict(B=-1),
-    dict(B=70000), dict(T=-1), dict(max_q=-1), dict(max_kv=-1), dict(max_kv=129), dict(MB=-1),
+    dict(H=65536, Hkv=1024), dict(B=70000), dict(T=-1), dict(max_q=-1), dict(max_kv=-1), dict(max_kv=129), dict(MB=-1),
     dict(MB=0, max_kv=0), dict(NB=0), dict(NB=-1), dict(scale=0.0), dict(scale=-1.0),
     dict(scale=NAN), dict(scale=INF), dict(partition=-2), dict(partition=64), dict(partition=200),
     dict(out=NULL), dict(q=NULL), dict(k=NULL), dict(v=NULL), dict(bt=NULL), dict(lens=NULL),
@@ -197,7 +197,8 @@ SHARED = dict(out=P, out_dt=binding.PA_BF16, q=P, k=P, v=P, bt=P, MB=64, seq=P, 
 
 @pytest.mark.parametrize("bad", [
     dict(D=96), dict(S=64), dict(S=4), dict(dt=binding.PA_F32), dict(out_dt=3), dict(H=0),
-    dict(Hkv=3), dict(H=1032, Hkv=8), dict(B=-1), dict(B=70000), dict(NG=-1), dict(NG=70000),
+    dict(Hkv=3), dict(H=1032, Hkv=8), dict(B=-1), dict(B=65535), dict(NG=-1), dict(NG=65535),
+    dict(H=65536, Hkv=1024),
     dict(NG=0), dict(max_group=0), dict(max_group=-1), dict(max_shared=-1), dict(max_tail=-1),
     dict(max_shared=1025), dict(max_tail=1025), dict(MB=0, max_shared=0, max_tail=0), dict(NB=0),
     dict(scale=0.0), dict(scale=NAN), dict(out=NULL), dict(q=NULL), dict(k=NULL), dict(v=NULL),

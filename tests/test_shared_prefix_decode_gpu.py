@@ -169,6 +169,27 @@ def test_extreme_scores_and_masked_infinities():
         assert bool(((out[i:i + 1] - want).abs() <= (30 * 2.0 ** -13 + 2.0 ** -17) * mag).all())
 
 
+@pytest.mark.parametrize("n", [3, 40])
+def test_nan_stays_nan_where_it_belongs(n):
+    """A NaN in a shared key makes NaN of its whole group, one in a tail of its request only;
+    padding rows of q may hold anything."""
+    lens = [300 + i for i in range(n)]
+    b = Batch([(256, lens), (128, [200, 0, 150])], 4, 4, 64, 16, torch.bfloat16, seed=n)
+    good = b.run()
+    b.q[n + 1] = float("nan")  # the request without tokens
+    out = b.run()
+    assert torch.equal(out, good) and bool((out[n + 1] == 0).all())
+    b.k[b.tables[1][17], 2, 5, 0] = float("nan")  # request 1's own token 277, head 2
+    out = b.run()
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[1, 2] = True
+    assert torch.equal(out.isnan(), want) and torch.equal(out[~want], good[~want])
+    b.k[b.tables[n][3], 0, 1, 9] = float("nan")  # a shared token of the second group, head 0
+    out = b.run()
+    want[n, 0] = want[n + 2, 0] = True
+    assert torch.equal(out.isnan(), want) and torch.equal(out[~want], good[~want])
+
+
 def test_equals_grouped_decode():
     """The same call without sharing (pa_decode_gqa) on a batch of forked sequences, through the
     allocator: tables of pa_seq_fork, a private last block after copy-on-write."""
