@@ -451,28 +451,21 @@ PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN, PA_ROPE_BANDS = range(
 
 def _one_device(names, tensors):
     """The index of the CUDA device that all the tensors (None: not given) are on."""
-    idx = -2
-    for n, t in enumerate(tensors):
-        if t is not None:
-            i = t.get_device()
-            if i != idx:
-                if i < 0:
-                    raise ValueError(f"{names[n]} must be a CUDA tensor")
-                if idx >= 0:
-                    raise ValueError(f"{names[n]} is on cuda:{i}, the others on cuda:{idx}")
-                idx = i
+    idx = tensors[0].get_device()
+    if idx < 0:
+        raise ValueError(f"{names[0]} must be a CUDA tensor")
+    for t in tensors:
+        if t is not None and t.get_device() != idx:
+            name = next(n for n, x in zip(names, tensors) if x is t)
+            if t.get_device() < 0:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, {names[0]} on cuda:{idx}")
     return idx
-
-
-def _all_contiguous(names, tensors):
-    for n, t in enumerate(tensors):
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{names[n]} must be contiguous")
 
 
 def _half_type(t, name):
     dt = t.dtype
-    if dt != torch.bfloat16 and dt != torch.float16:
+    if dt is not torch.bfloat16 and dt is not torch.float16:
         raise ValueError(f"{name} must be float16 or bfloat16")
     return dt
 
@@ -480,20 +473,23 @@ def _half_type(t, name):
 def _rows(t, name, T, D, dt):
     """(address, elements from one token to the next, heads) of t [T, heads, D]: tokens may be
     strided, the heads of a token are contiguous."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype != dt or len(shape) != 3 or shape[0] != T or shape[2] != D:
+    shape = t.shape
+    if t.dtype is not dt or len(shape) != 3 or shape[0] != T or shape[2] != D:
         raise ValueError(f"{name} must be {dt} [{T}, heads, {D}]".replace("torch.", ""))
     heads = shape[1]
-    if stride[2] != 1 or (stride[1] != D and heads > 1):
+    if t.is_contiguous():
+        return t.data_ptr(), heads * D, heads
+    step, head, one = t.stride()
+    if one != 1 or (head != D and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), stride[0] if T > 1 else heads * D, heads  # (one token has no next one)
+    return t.data_ptr(), step if T > 1 else heads * D, heads  # (one token has no next one)
 
 
 def _vector(t, name, n, dt):
     """The address of a contiguous vector of n elements (None: not given)."""
     if t is None:
         return None
-    if t.dtype != dt or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dt or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dt} [{n}]".replace("torch.", ""))
     return t.data_ptr()
 
@@ -613,14 +609,20 @@ def _paged_common(names, tensors):
     """Checks shared by pa_cross and pa_decode_shared (tensors in the order of their names);
     returns (device index, shapes of q and k_cache, their type, workspace address and bytes)."""
     idx = _one_device(names, tensors)
-    _all_contiguous(names, tensors)
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            name = next(n for n, x in zip(names, tensors) if x is t)
+            raise ValueError(f"{name} must be contiguous")
     out, q, k_cache, v_cache, block_tables, workspace = tensors[:6]
     dt = _half_type(q, "q")
     if k_cache.dtype != dt or v_cache.dtype != dt:
         raise ValueError("q and the caches must share one dtype")
-    for n in range(4, len(tensors)):
-        if n != 5 and tensors[n].dtype != torch.int32:
-            raise ValueError(f"{names[n]} must be int32")
+    for t in tensors[6:]:
+        if t.dtype is not torch.int32 or t.dim() != 1:
+            name = next(n for n, x in zip(names, tensors) if x is t)
+            raise ValueError(f"{name} must be an int32 vector")
+    if block_tables.dtype is not torch.int32:
+        raise ValueError("block_tables must be int32")
     if out.dtype not in _DT:
         raise ValueError("out must be float32, float16 or bfloat16")
     qs, cs = q.shape, k_cache.shape
@@ -647,8 +649,7 @@ def pa_cross(out, q, k_cache, v_cache, block_tables, kv_lens, q_start, scale, ma
     idx, (T, H, D), (NB, Hkv, S, _), dt, ws, ws_bytes = _paged_common(
         _CROSS_NAMES, (out, q, k_cache, v_cache, block_tables, workspace, kv_lens, q_start))
     B, MB = block_tables.shape
-    if kv_lens.dim() != 1 or kv_lens.numel() != B or q_start.dim() != 1 or \
-            q_start.numel() != B + 1:
+    if kv_lens.numel() != B or q_start.numel() != B + 1:
         raise ValueError("kv_lens must be [B] and q_start [B + 1]")
     _launch("pa_cross", idx, out.data_ptr(), _DT[out.dtype], q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), block_tables.data_ptr(), MB, kv_lens.data_ptr(),
@@ -671,8 +672,7 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, seq_lens, shared_le
         _SHARED_NAMES, (out, q, k_cache, v_cache, block_tables, workspace, seq_lens, shared_lens,
                         group_start))
     rows, MB = block_tables.shape
-    if rows != B or seq_lens.dim() != 1 or seq_lens.numel() != B or shared_lens.dim() != 1 or \
-            shared_lens.numel() != B or group_start.dim() != 1 or group_start.numel() < 1:
+    if rows != B or seq_lens.numel() != B or shared_lens.numel() != B or group_start.numel() < 1:
         raise ValueError("block_tables must be [B, MB], seq_lens and shared_lens [B], "
                          "group_start [NG + 1]")
     _launch("pa_decode_shared", idx, out.data_ptr(), _DT[out.dtype], q.data_ptr(),
