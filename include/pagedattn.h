@@ -374,7 +374,7 @@ pa_status pa_rope_append(void* q_out, int64_t q_out_stride, const void* q, int64
 /* The same into E4M3 caches (as pa_kv_append_fp8): k's rows are stored as the
  * codes of fp32(value / k_scale) of the 32-bit normed and rotated values (not
  * rounded to dt on the way), v's as pa_kv_append_fp8 stores them. D a
- * multiple of 16; scales finite and > 0. */
+ * multiple of 16; scales in [2^-60, 2^60]. */
 pa_status pa_rope_append_fp8(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                              const int32_t* positions, const int64_t* slot_mapping, void* k_cache,

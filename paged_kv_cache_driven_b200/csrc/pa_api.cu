@@ -931,8 +931,8 @@ pa_status pa_rope_append_fp8(void* q_out, int64_t q_out_stride, const void* q, i
                              const void* k_weight, float eps, int T, int H, int Hkv, int D, int S,
                              int NB, pa_dtype dt, void* stream) {
   if (D % 16 != 0) return PA_ERR_INVALID;  // as pa_kv_append_fp8: 16-byte cache rows
-  if (!(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
-    return PA_ERR_INVALID;
+  auto scale_ok = [](float s) { return s >= 0x1p-60f && s <= 0x1p60f; };
+  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return PA_ERR_INVALID;
   pa::RopeParams prm = rope_params(q_out, q_out_stride, q, q_stride, k, k_stride, positions, table,
                                    rot_dim, amplitude, q_weight, k_weight, eps, T, H, Hkv, D);
   prm.k_scale = k_scale;

@@ -129,7 +129,8 @@ def test_append_refusals(lib, bad):
     assert lib.pa_rope_append_fp8(*head, 1.0, 1.0, *tail) == INVALID
 
 
-@pytest.mark.parametrize("scales", [(0.0, 1.0), (1.0, -1.0), (NAN, 1.0), (1.0, INF)])
+@pytest.mark.parametrize("scales", [(0.0, 1.0), (1.0, -1.0), (NAN, 1.0), (1.0, INF), (1e-19, 1.0),
+                                    (1.0, 1e19)])
 def test_append_fp8_scales(lib, scales):
     v = list(APPEND.values())
     assert lib.pa_rope_append_fp8(*v[:12], *scales, *v[12:]) == INVALID

@@ -199,6 +199,38 @@ def test_append_e4m3(T, H, Hkv, D, S, rot, interleaved):
                            b.transpose(1, 2).reshape(NB * S, -1)[keep])
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+def test_every_value_over_many_scales(dt):
+    """Every 16-bit value, infinities and NaN among them, over scales of all kinds (powers of two,
+    mantissas of all ones, random ones, the ends of the range): v's codes are those of
+    pa_kv_append_fp8, whose quotients are correctly rounded divisions."""
+    Hkv, D, S = 4, 128, 16
+    T = 65536 // (Hkv * D)
+    v = torch.arange(65536, dtype=torch.int32, device=DEV).to(torch.int16).view(dt)
+    v = v.reshape(T, Hkv, D)
+    table = binding.pa_rope_table(D)[0].to(DEV)
+    pos = torch.zeros(T, dtype=torch.int32, device=DEV)
+    slots = torch.arange(T, device=DEV)
+    q = torch.zeros((T, 0, D), dtype=dt, device=DEV)
+    g = torch.Generator().manual_seed(0)
+    scales = [1.0, 0.5, 2.0 ** -9, 2.0 ** -60, 2.0 ** 60, 2.0 - 2.0 ** -23, 2.0 ** -7 - 2.0 ** -31,
+              1.0 + 2.0 ** -23, 3.0, 1.0 / 3.0]
+    scales += (2.0 ** (20 * torch.rand(120, generator=g, dtype=torch.float64) - 14)).tolist()
+    got, want = (torch.zeros((2, T // S, Hkv, S, D), dtype=torch.uint8, device=DEV)
+                 for _ in range(2))
+    for interleaved in (False, True):
+        for s in scales:
+            binding.pa_rope_append_fp8(q, q, v, v, pos, slots, got[0], got[1], s, s, table,
+                                       interleaved=interleaved)
+            binding.pa_kv_append_fp8(v, v, slots, want[0], want[1], s, s)
+            assert torch.equal(got[1], want[1]), s
+            # at position 0 the rotation changes no finite key
+            finite = v.isfinite().all(-1)
+            k = [c[0].transpose(1, 2).reshape(T, Hkv, D)[finite] for c in (got, want)]
+            k = [x.view(torch.float8_e4m3fn).float() for x in k]  # (-0 may become 0)
+            assert torch.equal(*k), s
+
+
 def test_bad_slots_are_skipped_and_flagged():
     q, k, v, (qw, kw) = inputs(4, 2, 2, 64, torch.bfloat16)
     table = binding.pa_rope_table(64)[0].to(DEV)
