@@ -455,6 +455,61 @@ pa_status pa_decode_shared(void* out, pa_dtype out_dt, const void* q, const void
                            int D, int S, int NB, pa_dtype dt, int max_group, int max_shared_len,
                            int max_tail_len, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Argument blocks: pa_rope, pa_rope_append(_fp8), pa_cross and pa_decode_shared
+ * with their arguments in one struct, in the order of the calls (the same checks
+ * and results), for bindings that pay for every argument they marshal: through
+ * ctypes the 22 arguments of pa_rope cost 2 us, a packed block 0.6.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  void* q_out;
+  int64_t q_out_stride;
+  void* k_out; /* pa_rope; ignored by the appends */
+  int64_t k_out_stride;
+  const void* q;
+  int64_t q_stride;
+  const void* k;
+  int64_t k_stride;
+  const void* v; /* the appends, with what follows up to the caches */
+  int64_t v_stride;
+  const int64_t* slot_mapping;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* positions;
+  const double* table;
+  const void* q_weight;
+  const void* k_weight;
+  void* stream;
+  float k_scale, v_scale; /* pa_rope_append_fp8 */
+  float amplitude, eps;
+  int32_t rot_dim, interleaved, T, H, Hkv, D, S, NB, dt;
+} pa_rope_args;
+
+pa_status pa_rope_call(const pa_rope_args* a);
+pa_status pa_rope_append_call(const pa_rope_args* a);
+pa_status pa_rope_append_fp8_call(const pa_rope_args* a);
+
+typedef struct {
+  void* out;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* lens;        /* kv_lens, or seq_lens */
+  const int32_t* start;       /* q_start, or group_start */
+  const int32_t* shared_lens; /* pa_decode_shared */
+  void* workspace;
+  uint64_t ws_bytes;
+  void* stream;
+  float scale;
+  int32_t out_dt, MB, B, H, Hkv, D, S, NB, dt;
+  int32_t T, max_q_len, max_kv_len, partition;            /* pa_cross */
+  int32_t NG, max_group, max_shared_len, max_tail_len;    /* pa_decode_shared */
+} pa_ranges_args;
+
+pa_status pa_cross_call(const pa_ranges_args* a);
+pa_status pa_decode_shared_call(const pa_ranges_args* a);
+
 /* Split-KV workspace layout, for tests that inspect the partition pass
  * (NP = number of partitions, n = B*H*NP, all fp32, offsets in bytes from
  * `workspace`):

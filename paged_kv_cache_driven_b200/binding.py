@@ -8,6 +8,7 @@ is no fallback.
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -90,6 +91,10 @@ _SIGNATURES = {
     "pa_decode_shared": ([_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32,
                           ctypes.c_float, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                           _i32, _vp, _sz, _vp], _i32),
+    # the last five with a packed argument block (_ROPE_ARGS, _RANGES_ARGS)
+    **{n: ([ctypes.c_char_p], _i32) for n in (
+        "pa_rope_call", "pa_rope_append_call", "pa_rope_append_fp8_call", "pa_cross_call",
+        "pa_decode_shared_call")},
     "pa_stepper_create": ([_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                            ctypes.c_float, _i32, _i32, _i32, _i32, _vp, _vp], _i32),
     "pa_stepper_destroy": ([_vp], None),
@@ -486,9 +491,9 @@ def _rows(t, name, T, D, dt):
 
 
 def _vector(t, name, n, dt):
-    """The address of a contiguous vector of n elements (None: not given)."""
+    """The address of a contiguous vector of n elements (0: not given)."""
     if t is None:
-        return None
+        return 0
     if t.dtype is not dt or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dt} [{n}]".replace("torch.", ""))
     return t.data_ptr()
@@ -498,16 +503,21 @@ def _raw_stream(idx, stream):
     return torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream
 
 
-def _launch(name, idx, *args):
-    """The entry point `name` with device `idx` current."""
+# pa_rope_args and pa_ranges_args (native alignment, as the C compiler lays them out)
+_ROPE_ARGS = struct.Struct("PqPqPqPqPqPPPPPPPP4f9i")
+_RANGES_ARGS = struct.Struct("9PQPf17i")
+
+
+def _launch(name, idx, block):
+    """The entry point `name` on its packed arguments, with device `idx` current."""
     fn = getattr(_lib or lib(), name)
     if torch._C._cuda_getDevice() == idx:
-        rc = fn(*args)
+        rc = fn(block)
     else:
         with torch.cuda.device(idx):
-            rc = fn(*args)
+            rc = fn(block)
     if rc != PA_OK:
-        raise PagedAttnError(rc, name)
+        raise PagedAttnError(rc, name[:-5])
 
 
 def pa_rope_table(rot_dim, base=10000.0, scaling=PA_ROPE_PLAIN, factor=1.0, low=1.0, high=32.0,
@@ -543,11 +553,12 @@ def pa_rope(q_out, k_out, q, k, positions, table, interleaved=False, amplitude=1
     if qoh != H or koh != Hkv:
         raise ValueError("q_out and k_out must have the heads of q and k")
     half = table.numel()
-    _launch("pa_rope", idx, qop, qos, kop, kos, qp, qs, kp, ks,
-            _vector(positions, "positions", T, torch.int32),
-            _vector(table, "table", half, torch.float64), 2 * half, 1 if interleaved else 0,
-            amplitude, _vector(q_weight, "q_weight", D, dt), _vector(k_weight, "k_weight", D, dt),
-            eps, T, H, Hkv, D, _DT[dt], _raw_stream(idx, stream))
+    _launch("pa_rope_call", idx, _ROPE_ARGS.pack(
+        qop, qos, kop, kos, qp, qs, kp, ks, 0, 0, 0, 0, 0,
+        _vector(positions, "positions", T, torch.int32),
+        _vector(table, "table", half, torch.float64), _vector(q_weight, "q_weight", D, dt),
+        _vector(k_weight, "k_weight", D, dt), _raw_stream(idx, stream), 0.0, 0.0, amplitude, eps,
+        2 * half, 1 if interleaved else 0, T, H, Hkv, D, 0, 0, _DT[dt]))
 
 
 def _rope_append(name, q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, scales, table,
@@ -571,13 +582,15 @@ def _rope_append(name, q_out, q, k, v, positions, slot_mapping, k_cache, v_cache
             not k_cache.is_contiguous() or not v_cache.is_contiguous():
         raise ValueError("the caches must be contiguous [NB, Hkv, S, D]")
     half = table.numel()
-    _launch(name, idx, qop, qos, qp, qs, kp, ks, vp, vs,
-            _vector(positions, "positions", T, torch.int32),
-            _vector(slot_mapping, "slot_mapping", T, torch.int64), k_cache.data_ptr(),
-            v_cache.data_ptr(), *scales, _vector(table, "table", half, torch.float64), 2 * half,
-            1 if interleaved else 0, amplitude, _vector(q_weight, "q_weight", D, dt),
-            _vector(k_weight, "k_weight", D, dt), eps, T, H, Hkv, D, shape[2], shape[0], _DT[dt],
-            _raw_stream(idx, stream))
+    k_scale, v_scale = scales or (0.0, 0.0)
+    _launch(name, idx, _ROPE_ARGS.pack(
+        qop, qos, 0, 0, qp, qs, kp, ks, vp, vs,
+        _vector(slot_mapping, "slot_mapping", T, torch.int64), k_cache.data_ptr(),
+        v_cache.data_ptr(), _vector(positions, "positions", T, torch.int32),
+        _vector(table, "table", half, torch.float64), _vector(q_weight, "q_weight", D, dt),
+        _vector(k_weight, "k_weight", D, dt), _raw_stream(idx, stream), k_scale, v_scale,
+        amplitude, eps, 2 * half, 1 if interleaved else 0, T, H, Hkv, D, shape[2], shape[0],
+        _DT[dt]))
 
 
 def pa_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, table,
@@ -586,7 +599,7 @@ def pa_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, ta
     """pa_rope of q into q_out and of k into k_cache, with v into v_cache, at slot_mapping [T]
     (int64; negative slots skip a token's k and v): one pass instead of pa_rope and pa_kv_append,
     the same bits."""
-    _rope_append("pa_rope_append", q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, (),
+    _rope_append("pa_rope_append_call", q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, (),
                  table, interleaved, amplitude, q_weight, k_weight, eps, stream)
 
 
@@ -594,7 +607,7 @@ def pa_rope_append_fp8(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache
                        table, interleaved=False, amplitude=1.0, q_weight=None, k_weight=None,
                        eps=1e-6, stream=None):
     """pa_rope_append into uint8 E4M3 caches: codes of fp32(value / scale)."""
-    _rope_append("pa_rope_append_fp8", q_out, q, k, v, positions, slot_mapping, k_cache, v_cache,
+    _rope_append("pa_rope_append_fp8_call", q_out, q, k, v, positions, slot_mapping, k_cache, v_cache,
                  (k_scale, v_scale), table, interleaved, amplitude, q_weight, k_weight, eps,
                  stream)
 
@@ -633,7 +646,7 @@ def _paged_common(names, tensors):
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be [B, MB]")
     if workspace is None:
-        return idx, qs, cs, dt, None, 0
+        return idx, qs, cs, dt, 0, 0
     return idx, qs, cs, dt, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -651,10 +664,11 @@ def pa_cross(out, q, k_cache, v_cache, block_tables, kv_lens, q_start, scale, ma
     B, MB = block_tables.shape
     if kv_lens.numel() != B or q_start.numel() != B + 1:
         raise ValueError("kv_lens must be [B] and q_start [B + 1]")
-    _launch("pa_cross", idx, out.data_ptr(), _DT[out.dtype], q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), block_tables.data_ptr(), MB, kv_lens.data_ptr(),
-            q_start.data_ptr(), scale, B, H, Hkv, D, S, NB, _DT[dt], T, max_q_len, max_kv_len,
-            partition, ws, ws_bytes, _raw_stream(idx, stream))
+    _launch("pa_cross_call", idx, _RANGES_ARGS.pack(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_tables.data_ptr(), kv_lens.data_ptr(), q_start.data_ptr(), 0, ws, ws_bytes,
+        _raw_stream(idx, stream), scale, _DT[out.dtype], MB, B, H, Hkv, D, S, NB, _DT[dt], T,
+        max_q_len, max_kv_len, partition, 0, 0, 0, 0))
 
 
 def pa_decode_shared_workspace_bytes(B, NG, H, Hkv, D, S, max_group, max_shared_len,
@@ -675,11 +689,12 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, seq_lens, shared_le
     if rows != B or seq_lens.numel() != B or shared_lens.numel() != B or group_start.numel() < 1:
         raise ValueError("block_tables must be [B, MB], seq_lens and shared_lens [B], "
                          "group_start [NG + 1]")
-    _launch("pa_decode_shared", idx, out.data_ptr(), _DT[out.dtype], q.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), MB,
-            seq_lens.data_ptr(), shared_lens.data_ptr(), group_start.data_ptr(),
-            group_start.numel() - 1, scale, B, H, Hkv, D, S, NB, _DT[dt], max_group,
-            max_shared_len, max_tail_len, ws, ws_bytes, _raw_stream(idx, stream))
+    _launch("pa_decode_shared_call", idx, _RANGES_ARGS.pack(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_tables.data_ptr(), seq_lens.data_ptr(), group_start.data_ptr(),
+        shared_lens.data_ptr(), ws, ws_bytes, _raw_stream(idx, stream), scale, _DT[out.dtype], MB,
+        B, H, Hkv, D, S, NB, _DT[dt], 0, 0, 0, 0, group_start.numel() - 1, max_group,
+        max_shared_len, max_tail_len))
 
 
 def pa_copy_blocks(k_cache, v_cache, src_dst, stream=None):

@@ -1277,3 +1277,54 @@ pa_status pa_decode_shared(void* out, pa_dtype out_dt, const void* q, const void
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The same calls on argument blocks.
+// ---------------------------------------------------------------------------
+
+extern "C" {
+
+pa_status pa_rope_call(const pa_rope_args* a) {
+  if (!a) return PA_ERR_INVALID;
+  return pa_rope(a->q_out, a->q_out_stride, a->k_out, a->k_out_stride, a->q, a->q_stride, a->k,
+                 a->k_stride, a->positions, a->table, a->rot_dim, a->interleaved, a->amplitude,
+                 a->q_weight, a->k_weight, a->eps, a->T, a->H, a->Hkv, a->D,
+                 static_cast<pa_dtype>(a->dt), a->stream);
+}
+
+pa_status pa_rope_append_call(const pa_rope_args* a) {
+  if (!a) return PA_ERR_INVALID;
+  return pa_rope_append(a->q_out, a->q_out_stride, a->q, a->q_stride, a->k, a->k_stride, a->v,
+                        a->v_stride, a->positions, a->slot_mapping, a->k_cache, a->v_cache,
+                        a->table, a->rot_dim, a->interleaved, a->amplitude, a->q_weight,
+                        a->k_weight, a->eps, a->T, a->H, a->Hkv, a->D, a->S, a->NB,
+                        static_cast<pa_dtype>(a->dt), a->stream);
+}
+
+pa_status pa_rope_append_fp8_call(const pa_rope_args* a) {
+  if (!a) return PA_ERR_INVALID;
+  return pa_rope_append_fp8(a->q_out, a->q_out_stride, a->q, a->q_stride, a->k, a->k_stride, a->v,
+                            a->v_stride, a->positions, a->slot_mapping, a->k_cache, a->v_cache,
+                            a->k_scale, a->v_scale, a->table, a->rot_dim, a->interleaved,
+                            a->amplitude, a->q_weight, a->k_weight, a->eps, a->T, a->H, a->Hkv,
+                            a->D, a->S, a->NB, static_cast<pa_dtype>(a->dt), a->stream);
+}
+
+pa_status pa_cross_call(const pa_ranges_args* a) {
+  if (!a) return PA_ERR_INVALID;
+  return pa_cross(a->out, static_cast<pa_dtype>(a->out_dt), a->q, a->k_cache, a->v_cache,
+                  a->block_tables, a->MB, a->lens, a->start, a->scale, a->B, a->H, a->Hkv, a->D,
+                  a->S, a->NB, static_cast<pa_dtype>(a->dt), a->T, a->max_q_len, a->max_kv_len,
+                  a->partition, a->workspace, a->ws_bytes, a->stream);
+}
+
+pa_status pa_decode_shared_call(const pa_ranges_args* a) {
+  if (!a) return PA_ERR_INVALID;
+  return pa_decode_shared(a->out, static_cast<pa_dtype>(a->out_dt), a->q, a->k_cache, a->v_cache,
+                          a->block_tables, a->MB, a->lens, a->shared_lens, a->start, a->NG,
+                          a->scale, a->B, a->H, a->Hkv, a->D, a->S, a->NB,
+                          static_cast<pa_dtype>(a->dt), a->max_group, a->max_shared_len,
+                          a->max_tail_len, a->workspace, a->ws_bytes, a->stream);
+}
+
+}  // extern "C"

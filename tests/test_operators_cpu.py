@@ -92,6 +92,29 @@ def test_table_refusals(lib, bad):
     assert lib.pa_rope_table(NULL, 64, 1e4, 0, 1.0, 1.0, 2.0, 0.0, ctypes.byref(amp)) == INVALID
 
 
+def address(x):
+    return 0 if x is None else x.value if isinstance(x, ctypes.c_void_p) else x
+
+
+def rope_block(a, scales=(1.0, 1.0)):
+    """The arguments of a rotary call as an argument block."""
+    ptr = ["q_out", "qos", "k_out", "kos", "q", "qs", "k", "ks", "v", "vs", "slots", "kc", "vc",
+           "pos", "table", "qw", "kw", "stream"]
+    return binding._ROPE_ARGS.pack(
+        *(address(a.get(n)) for n in ptr), *scales, a["amp"], a["eps"],
+        *(a.get(n, 0) for n in ("rot", "il", "T", "H", "Hkv", "D", "S", "NB", "dt")))
+
+
+def ranges_block(a):
+    """The arguments of pa_cross or pa_decode_shared as an argument block."""
+    a = {**a, "lens": a.get("lens", a.get("seq"))}
+    ptr = ["out", "q", "k", "v", "bt", "lens", "start", "sh", "ws", "ws_bytes", "stream"]
+    ints = ["out_dt", "MB", "B", "H", "Hkv", "D", "S", "NB", "dt", "T", "max_q", "max_kv",
+            "partition", "NG", "max_group", "max_shared", "max_tail"]
+    return binding._RANGES_ARGS.pack(*(address(a.get(n)) for n in ptr), a["scale"],
+                                     *(a.get(n, 0) for n in ints))
+
+
 ROPE = dict(q_out=P, qos=4 * 64, k_out=P, kos=2 * 64, q=P, qs=4 * 64, k=P, ks=2 * 64, pos=P,
             table=P, rot=64, il=0, amp=1.0, qw=NULL, kw=NULL, eps=1e-6, T=3, H=4, Hkv=2, D=64,
             dt=binding.PA_BF16, stream=NULL)
@@ -106,11 +129,17 @@ ROPE = dict(q_out=P, qos=4 * 64, k_out=P, kos=2 * 64, q=P, qs=4 * 64, k=P, ks=2 
     dict(qos=-256), dict(table=ctypes.c_void_p(16 * 1024 + 4)), dict(H=2 ** 29, qs=2 ** 36)])
 def test_rope_refusals(lib, bad):
     assert lib.pa_rope(*{**ROPE, **bad}.values()) == INVALID
+    assert lib.pa_rope_call(rope_block({**ROPE, **bad})) == INVALID
 
 
 def test_rope_without_work(lib):
     assert lib.pa_rope(*{**ROPE, "T": 0, "q": NULL, "pos": NULL}.values()) == OK
     assert lib.pa_rope(*{**ROPE, "H": 0, "Hkv": 0, "q": NULL}.values()) == OK
+    for none in (dict(T=0, q=NULL), dict(H=0, Hkv=0, k=NULL)):
+        assert lib.pa_rope_call(rope_block({**ROPE, **none})) == OK
+    for name in ("pa_rope_call", "pa_rope_append_call", "pa_rope_append_fp8_call",
+                 "pa_cross_call", "pa_decode_shared_call"):
+        assert getattr(lib, name)(None) == INVALID
 
 
 APPEND = dict(q_out=P, qos=4 * 64, q=P, qs=4 * 64, k=P, ks=2 * 64, v=P, vs=2 * 64, pos=P, slots=P,
@@ -127,6 +156,10 @@ def test_append_refusals(lib, bad):
     assert lib.pa_rope_append(*args.values()) == INVALID
     head, tail = list(args.values())[:12], list(args.values())[12:]
     assert lib.pa_rope_append_fp8(*head, 1.0, 1.0, *tail) == INVALID
+    assert lib.pa_rope_append_call(rope_block(args)) == INVALID
+    assert lib.pa_rope_append_fp8_call(rope_block(args)) == INVALID
+    for name in ("pa_rope_append_call", "pa_rope_append_fp8_call"):  # (the block itself is good)
+        assert getattr(lib, name)(rope_block({**APPEND, "T": 0})) == OK
 
 
 @pytest.mark.parametrize("scales", [(0.0, 1.0), (1.0, -1.0), (NAN, 1.0), (1.0, INF), (1e-19, 1.0),
@@ -134,6 +167,7 @@ def test_append_refusals(lib, bad):
 def test_append_fp8_scales(lib, scales):
     v = list(APPEND.values())
     assert lib.pa_rope_append_fp8(*v[:12], *scales, *v[12:]) == INVALID
+    assert lib.pa_rope_append_fp8_call(rope_block(APPEND, scales)) == INVALID
     v = list({**APPEND, "D": 72, "qs": 288, "ks": 144, "vs": 144, "qos": 288}.values())
     assert lib.pa_rope_append_fp8(*v[:12], 1.0, 1.0, *v[12:]) == INVALID  # D % 16
     v = list({**APPEND, "T": 0}.values())
@@ -160,11 +194,13 @@ CROSS = dict(out=P, out_dt=binding.PA_F32, q=P, k=P, v=P, bt=P, MB=8, lens=P, st
     dict(MB=64, max_kv=1000, partition=128, ws=ODD, ws_bytes=2 ** 40)])
 def test_cross_refusals(lib, bad):
     assert lib.pa_cross(*{**CROSS, **bad}.values()) == INVALID
+    assert lib.pa_cross_call(ranges_block({**CROSS, **bad})) == INVALID
 
 
 def test_cross_without_work(lib):
     for none in (dict(B=0), dict(T=0), dict(max_q=0)):
         assert lib.pa_cross(*{**CROSS, **none, "q": NULL, "out": NULL}.values()) == OK
+        assert lib.pa_cross_call(ranges_block({**CROSS, **none, "q": NULL})) == OK
 
 
 def slots(n_bytes, pairs, D):
@@ -208,11 +244,13 @@ SHARED = dict(out=P, out_dt=binding.PA_BF16, q=P, k=P, v=P, bt=P, MB=64, seq=P, 
     dict(NB=2 ** 28), dict(MB=2 ** 28)])
 def test_shared_refusals(lib, bad):
     assert lib.pa_decode_shared(*{**SHARED, **bad}.values()) == INVALID
+    assert lib.pa_decode_shared_call(ranges_block({**SHARED, **bad})) == INVALID
 
 
 def test_shared_without_work(lib):
     assert lib.pa_decode_shared(*{**SHARED, "B": 0, "NG": 0, "q": NULL, "ws": NULL,
                                   "ws_bytes": 0}.values()) == OK
+    assert lib.pa_decode_shared_call(ranges_block({**SHARED, "B": 0, "NG": 0, "ws": NULL})) == OK
 
 
 def test_shared_workspace(lib):
