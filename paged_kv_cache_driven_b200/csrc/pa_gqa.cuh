@@ -229,15 +229,25 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
   int width = p.MB;  // entries of the table row from trow on
   constexpr bool TAIL = std::is_same<Prm, DecodeParamsTail>::value;
   constexpr bool FAST = FEW || TAIL;
+  int ids_a = -1, ids_b = -1;
+  auto load_ids = [&](int blk1) {
+    const int lim = min(blk1, width);
+    ids_a = (blk0 + lane < lim) ? __ldg(trow + blk0 + lane) : -1;
+    ids_b = (blk0 + 32 + lane < lim) ? __ldg(trow + blk0 + 32 + lane) : -1;
+  };
   int L = 0;
   bool grouped = false;  // FEW: the shared part of a group of requests
   if constexpr (FEW) grouped = p.shared_lens != nullptr;
   if (!grouped) L = __ldg(p.seq_lens + i);
   if constexpr (FEW) {
     if (grouped) {
-      // the longest shared part of the requests served here, through that request's table
-      int who = q0 + c0 / G;
-      const int tok = q0 + c0 / G + lane;
+      // the longest shared part of the requests served here, through that
+      // request's table; mostly the first one's, which is asked for meanwhile
+      const int first = q0 + c0 / G;
+      trow = p.block_tables + static_cast<int64_t>(first) * p.MB;
+      if (w == NC) load_ids(blk0 + p.P / S);
+      int who = first;
+      const int tok = first + lane;
       if (tok <= q0 + (c0 + gc - 1) / G) {
         const int sh = __ldg(p.shared_lens + tok), len = __ldg(p.seq_lens + tok);
         if (w == 0 && part == 0 && hk == 0 && (sh < 0 || sh > p.L_cap || len < 0))
@@ -250,7 +260,10 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
         const int e = __shfl_xor_sync(kFullMask, L, o), b = __shfl_xor_sync(kFullMask, who, o);
         if (e > L || (e == L && b < who)) L = e, who = b;
       }
-      trow = p.block_tables + static_cast<int64_t>(who) * p.MB;
+      if (who != first) {
+        trow = p.block_tables + static_cast<int64_t>(who) * p.MB;
+        if (w == NC) load_ids(blk0 + p.P / S);
+      }
     }
   }
   if constexpr (TAIL) {
@@ -263,13 +276,7 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
     trow += skip / S;
     width -= skip / S;
   }
-  int ids_a = -1, ids_b = -1;
-  auto load_ids = [&](int blk1) {
-    const int lim = min(blk1, width);
-    ids_a = (blk0 + lane < lim) ? __ldg(trow + blk0 + lane) : -1;
-    ids_b = (blk0 + 32 + lane < lim) ? __ldg(trow + blk0 + 32 + lane) : -1;
-  };
-  if (w == NC) load_ids(blk0 + p.P / S);
+  if (w == NC && !grouped) load_ids(blk0 + p.P / S);
   const bool len_ok = L >= 0 && L <= p.L_cap;
   if (!len_ok) {
     if (threadIdx.x == 0 && part == 0 && blockIdx.y == 0) raise_error(PA_DEVERR_SEQ_LEN);

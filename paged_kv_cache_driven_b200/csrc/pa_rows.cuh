@@ -781,8 +781,21 @@ __device__ __forceinline__ void merge_row(const float* ws_m, const float* ws_l,
   const float* acc = ws_acc + ih * NP * D + lane * DL;
   const int n = na + nb;
   auto slot_of = [&](int q) { return q < na ? a0 + q : b0 + (q - na); };
-  float M = -INFINITY;
-  for (int q = lane; q < n; q += 32) M = fmaxf(M, m[slot_of(q)]);
+  // the first results' rows and everyone's m and l are asked for together
+  constexpr int FIRST = D == 256 ? 4 : 8;
+  float2 v0[FIRST][DL / 2];
+#pragma unroll
+  for (int r = 0; r < FIRST; ++r)
+    if (r < n) {
+#pragma unroll
+      for (int e = 0; e < DL / 2; ++e)
+        v0[r][e] = reinterpret_cast<const float2*>(
+            acc + static_cast<int64_t>(slot_of(r)) * D)[e];
+    }
+  const float m0 = lane < n ? m[slot_of(lane)] : -INFINITY;
+  const float l0 = lane < n ? l[slot_of(lane)] : 0.f;
+  float M = m0;
+  for (int q = lane + 32; q < n; q += 32) M = fmaxf(M, m[slot_of(q)]);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
   float lsum = 0.f, a[DL];
@@ -792,13 +805,26 @@ __device__ __forceinline__ void merge_row(const float* ws_m, const float* ws_l,
     const int q = c + lane;
     float wq = 0.f;
     if (q < n) {
-      const float mq = m[slot_of(q)];
+      const float mq = c == 0 ? m0 : m[slot_of(q)];
       wq = mq == -INFINITY ? 0.f : exp2f(mq - M);
-      lsum = fmaf(wq, l[slot_of(q)], lsum);
+      lsum = fmaf(wq, c == 0 ? l0 : l[slot_of(q)], lsum);
     }
     const int lim = min(32, n - c);
+    if (c == 0) {
+#pragma unroll
+      for (int r = 0; r < FIRST; ++r) {
+        const float w = __shfl_sync(kFullMask, wq, r);
+        if (r < n) {
+#pragma unroll
+          for (int e = 0; e < DL / 2; ++e) {
+            a[2 * e] = fmaf(w, v0[r][e].x, a[2 * e]);
+            a[2 * e + 1] = fmaf(w, v0[r][e].y, a[2 * e + 1]);
+          }
+        }
+      }
+    }
 #pragma unroll 4
-    for (int r = 0; r < lim; ++r) {
+    for (int r = c == 0 ? FIRST : 0; r < lim; ++r) {
       const float w = __shfl_sync(kFullMask, wq, r);
       const float* row = acc + static_cast<int64_t>(slot_of(c + r)) * D;
 #pragma unroll
