@@ -991,11 +991,18 @@ RowsPlan plan_few(int items, int Hkv, int D, int max_len, int partition) {
 // and KV head go to the grouped-query kernel (plan_few), whose small CTAs share
 // an SM: 8 single tokens on 20 heads over up to 1,500 keys took 30.9 us on the
 // rows kernel. The rest goes to the rows kernel: `items` with up to max_rows query
-// tokens each, G heads per KV head, keys up to max_len. The choice minimises an
-// estimate of the time, in units of one key tile with both halves on one row
-// tile: waves of CTAs (one per SM) x (key tiles per CTA x the tile's time + a
-// CTA's start and end), plus, where the keys are split, the merge.
-RowsPlan plan_rows(int items, int max_rows, int G, int Hkv, int D, int max_len, int partition) {
+// tokens each, G heads per KV head, keys up to max_len.
+//
+// The choice minimises an estimate of the time, in units of 1.2 us: waves of CTAs
+// x (key tiles per CTA x a tile's time + 4 for a CTA's start and end), plus,
+// where the keys are split, the merge. `behind` is the time of the work that may
+// run beside it (the tails of pa_decode_shared; 0 for pa_cross): it proceeds on the
+// SMs that one wave leaves free, at up to 1.3 times their share (what bounds it is
+// HBM), and what then remains of it follows. Leaving SMs free pays: 64 requests
+// behind 2,048 tokens on 40 heads 69.3 us with 120 CTAs for the shared part, 65.0
+// with 40; 24 behind 4,000 on 32/8 heads 32.3 us with 128 CTAs, 22.4 with 64.
+RowsPlan plan_rows(int items, int max_rows, int G, int Hkv, int D, int max_len, int partition,
+                   double behind) {
   if (static_cast<int64_t>(max_rows) * G <= 16)
     return plan_few(items, Hkv, D, max_len, partition);
   const int64_t tiles = std::max<int64_t>(1, ceil_div(max_len, kKeyTile));
@@ -1009,7 +1016,7 @@ RowsPlan plan_rows(int items, int max_rows, int G, int Hkv, int D, int max_len, 
   for (int split = D == 128 ? 1 : 0; split >= 0; --split) {
     const int row_tiles = (split || D != 128) ? 1 : 2;
     if (row_tiles == 2 && max_rows <= qpt) continue;  // nothing for the second half
-    const double tile_cost = split ? 1.0 : 2.0;
+    const double tile_cost = split ? 1.0 : (D == 256 ? 3.0 : 2.0);
     const int64_t ctas = static_cast<int64_t>(std::max(items, 1)) * Hkv *
                          std::max<int64_t>(1, ceil_div(max_rows, row_tiles * qpt));
     const int64_t most =
@@ -1019,9 +1026,14 @@ RowsPlan plan_rows(int items, int max_rows, int G, int Hkv, int D, int max_len, 
       if (partition > 0) per = partition / kKeyTile;
       const int64_t parts = ceil_div(tiles, per);
       const int64_t waves = ceil_div(ctas * parts, slots);
-      double cost = static_cast<double>(waves) * (per * tile_cost + 2.0);
-      if (parts > 1)  // the merge: its launch, and its reads and writes of the results
-        cost += 1.5 + static_cast<double>(items) * max_rows * Hkv * G * parts * D * 8.0 / 9.0e6;
+      double cost = static_cast<double>(waves) * (per * tile_cost + 4.0);
+      if (behind > 0.0) {
+        const double free = std::max(0.0, 1.0 - static_cast<double>(ctas * parts) / slots);
+        cost += std::max(0.0, behind - std::min(1.0, 1.3 * free) * cost);
+      }
+      if (parts > 1)  // the merge: its launch (or a part more), its reads and writes
+        cost += (behind > 0.0 ? 0.1 * parts : 1.5) +
+                static_cast<double>(items) * max_rows * Hkv * G * parts * D * 8.0 / 9.0e6;
       if (!any || cost < best_cost) {
         any = true;
         best_cost = cost;
@@ -1032,6 +1044,17 @@ RowsPlan plan_rows(int items, int max_rows, int G, int Hkv, int D, int max_len, 
     }
   }
   return best;
+}
+
+// The time of the tails' pass in the same units: their bytes (half of the bound on
+// average) at HBM's rate, at least one CTA's time (2.9) for each wave of CTAs.
+double tail_time(int B, int H, int Hkv, int D, int S, int max_tail_len, int parts) {
+  if (parts <= 0 || B <= 0) return 0.0;
+  const int G = H / Hkv;
+  const double bytes = static_cast<double>(B) * (0.5 * max_tail_len + 0.5 * S) * Hkv * D * 4.0;
+  const int64_t per_sm = G == 1 ? (D == 64 ? 6 : 3) : (D == 64 ? 7 : (D == 128 ? 4 : 2));
+  const int64_t ctas = static_cast<int64_t>(B) * parts * (G == 1 ? H : Hkv * ((G + 15) / 16));
+  return std::max(bytes / 7.8e6, 2.9 * ceil_div(ctas, per_sm * sm_count()));
 }
 
 // (P is then at most INT_MAX)
@@ -1083,11 +1106,12 @@ struct SharedPlan {
 SharedPlan plan_shared(int B, int NG, int H, int Hkv, int D, int S, int max_group,
                        int max_shared_len, int max_tail_len) {
   SharedPlan s{};
-  s.rows = plan_rows(NG, max_group, H / Hkv, Hkv, D, max_shared_len, 0);
-  s.shared_parts = max_shared_len > 0 ? s.rows.parts : 0;
   int P = 0, NP = 1;
   plan_grouped(B, H, Hkv, S, max_tail_len, 0, &P, &NP);
   s.tail_parts = max_tail_len > 0 ? NP : 0;
+  s.rows = plan_rows(NG, max_group, H / Hkv, Hkv, D, max_shared_len, 0,
+                     tail_time(B, H, Hkv, D, S, max_tail_len, s.tail_parts));
+  s.shared_parts = max_shared_len > 0 ? s.rows.parts : 0;
   s.tail_P = P > 0 ? P : static_cast<int>(ceil_div(std::max(max_tail_len, 1), S) * S);
   return s;
 }
@@ -1109,7 +1133,8 @@ size_t pa_cross_workspace_bytes(int B, int T, int H, int Hkv, int D, int max_q_l
   if (B <= 0 || T <= 0 || max_q_len <= 0 || !rows_len_ok(max_kv_len) || !rows_shape_ok(H, Hkv, D))
     return 0;
   if (partition < -1 || (partition > 0 && partition % kKeyTile != 0)) return 0;
-  const RowsPlan pl = plan_rows(B, std::min(max_q_len, T), H / Hkv, Hkv, D, max_kv_len, partition);
+  const RowsPlan pl = plan_rows(B, std::min(max_q_len, T), H / Hkv, Hkv, D, max_kv_len, partition,
+                                0.0);
   return workspace_for(T, H, D, pl.parts);
 }
 
@@ -1134,7 +1159,7 @@ pa_status pa_cross(void* out, pa_dtype out_dt, const void* q, const void* k_cach
   if (B > 65535 || NB == 0 || static_cast<int64_t>(NB) * Hkv * S > INT_MAX) return PA_ERR_INVALID;
   const int G = H / Hkv;
   const int max_rows = std::min(max_q_len, T);
-  const RowsPlan pl = plan_rows(B, max_rows, G, Hkv, D, max_kv_len, partition);
+  const RowsPlan pl = plan_rows(B, max_rows, G, Hkv, D, max_kv_len, partition, 0.0);
   // grid: x row tiles and KV heads (merge: row and head pairs), y partitions
   if (static_cast<int64_t>(max_rows) * H > INT_MAX || pl.parts > 65535) return PA_ERR_INVALID;
   const size_t need = workspace_for(T, H, D, pl.parts);

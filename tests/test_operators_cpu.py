@@ -256,10 +256,14 @@ def test_shared_without_work(lib):
 def test_shared_workspace(lib):
     ws = binding.pa_decode_shared_workspace_bytes
     # the shared part's slots, then the tails' (one where nothing splits them)
-    both = slots(ws(64, 1, 40, 40, 128, 16, 64, 2048, 100), 64 * 40, 128)
     tails = slots(ws(64, 1, 40, 40, 128, 16, 64, 0, 100), 64 * 40, 128)
-    assert tails == 1 and both > tails
-    assert slots(ws(64, 1, 40, 40, 128, 16, 64, 2048, 0), 64 * 40, 128) == both - tails
+    alone = slots(ws(64, 1, 40, 40, 128, 16, 64, 2048, 0), 64 * 40, 128)
+    both = slots(ws(64, 1, 40, 40, 128, 16, 64, 2048, 100), 64 * 40, 128)
+    # alone the shared part is cut to fill the SMs (3 x 40 CTAs of 148); beside tails it leaves
+    # some to them
+    assert (tails, alone) == (1, 3) and tails < both < tails + alone
+    # 64 query heads on 8 KV heads, 512 rows: two CTAs of two row tiles per KV head and part
+    assert slots(ws(64, 1, 64, 8, 128, 16, 64, 32768, 0), 64 * 64, 128) == 9
     assert ws(64, 1, 40, 40, 128, 16, 64, 0, 0) == 0
     assert ws(0, 0, 40, 40, 128, 16, 64, 2048, 100) == 0
     assert ws(4, 1, 40, 40, 96, 16, 64, 2048, 100) == 0
