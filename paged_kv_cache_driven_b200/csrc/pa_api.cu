@@ -1016,7 +1016,7 @@ RowsPlan plan_rows(int items, int max_rows, int G, int Hkv, int D, int max_len, 
   for (int split = D == 128 ? 1 : 0; split >= 0; --split) {
     const int row_tiles = (split || D != 128) ? 1 : 2;
     if (row_tiles == 2 && max_rows <= qpt) continue;  // nothing for the second half
-    const double tile_cost = split ? 1.0 : (D == 256 ? 3.0 : 2.0);
+    const double tile_cost = split ? 1.0 : (D == 256 ? 3.0 : (D == 64 ? 1.6 : 2.0));
     const int64_t ctas = static_cast<int64_t>(std::max(items, 1)) * Hkv *
                          std::max<int64_t>(1, ceil_div(max_rows, row_tiles * qpt));
     const int64_t most =

@@ -16,6 +16,14 @@ pa_status launch(const RowsParams& prm, const void* q, cudaStream_t stream) {
   using Tl = RowsTiling<D, KSPLIT>;
   auto kern = rows_kernel<T, D, KSPLIT>;
   static bool configured[kMaxDevices] = {};
+  if constexpr (Tl::PASS_REGS) {
+    // the softmax warps would wait for good for registers the launch did not bring
+    static const int regs = [&] {
+      cudaFuncAttributes at = {};
+      return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs < Tl::LAUNCH_REGS) return PA_ERR_CUDA;
+  }
   if (!opt_in_smem(kern, Tl::SMEM, configured)) return PA_ERR_CUDA;
   const pa_dtype dt = std::is_same<T, __half>::value ? PA_F16 : PA_BF16;
   const int64_t rows = static_cast<int64_t>(prm.NB) * prm.Hkv * prm.S;
@@ -32,7 +40,7 @@ pa_status launch(const RowsParams& prm, const void* q, cudaStream_t stream) {
 
 template <typename T>
 pa_status by_size(const RowsParams& prm, const void* q, int D, bool split_keys, cudaStream_t st) {
-  if (D == 64) return launch<T, 64, false>(prm, q, st);
+  if (D == 64) return launch<T, 64, true>(prm, q, st);
   if (D == 128)
     return split_keys ? launch<T, 128, true>(prm, q, st) : launch<T, 128, false>(prm, q, st);
   if (D == 256) return launch<T, 256, false>(prm, q, st);

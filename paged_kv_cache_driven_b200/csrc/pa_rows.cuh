@@ -12,10 +12,11 @@
 // block (box 64 x G heads x qpt tokens), row r = token r / G, head r % G. K and V
 // are thus read once for all of a tile's tokens and heads.
 //
-// One CTA per (row tiles, KV head, partition of the keys, item), up to 640 threads in the roles of the causal prefill kernel: two softmax
-// warpgroups per stream, producer warps (one lane per cache block and TMA box),
-// an MMA issuer warp that also owns tensor memory. Two streams ping-pong, so
-// that the tensor cores work for one while the other's softmax runs:
+// One CTA per (row tiles, KV head, partition of the keys, item), up to 640 threads
+// in the roles of the causal prefill kernel: two softmax warpgroups per stream (one
+// at head size 64), producer warps (one lane per cache block and TMA box), an MMA
+// issuer warp that also owns tensor memory. Two streams ping-pong, so that the
+// tensor cores work for one while the other's softmax runs:
 //   KSPLIT = false  stream t takes row tile t: both read every key tile;
 //   KSPLIT = true   one row tile (few rows): stream t takes the key tiles
 //                   t, t + 2, ..., and the CTA joins the two results at its end
@@ -41,15 +42,21 @@ namespace pa {
 template <int D, bool KSPLIT>
 struct RowsTiling {
   static constexpr int BM = 128;              // query rows per tile (MMA M)
-  static constexpr int BN = 128;              // keys per tile
-  // Streams: two at head size 128. One at head size 256, which fills tensor and
-  // shared memory, and at head size 64, where two CTAs share an SM instead
-  // (256 tensor-memory columns and some 85 KB each) and also cover each other's
-  // start and end (16 ragged prompts on 32 heads: 115 us with two streams per CTA).
-  static constexpr int NST = D == 128 ? 2 : 1;
+  static constexpr int BN = D == 64 ? 64 : 128;  // keys per tile
+  // Streams: two, or one at head size 256, which fills tensor and shared memory.
+  // At head size 64 two CTAs share an SM (256 tensor-memory columns and some 85 KB
+  // each) and cover each other's start and end, and a stream is one warpgroup with
+  // tiles of 64 keys, whose threads hold whole rows: four chains of product,
+  // softmax, product are then under way on an SM, and none waits for another's
+  // row maximum. 128 rows x 128 keys take 0.95 us of an SM in bf16, 0.80 in f16,
+  // where two chains of two warpgroups each took 1.16 and 0.89 (16 ragged prompts on
+  // 32 heads 117.4 -> 98.7 us; a CTA's end, which joins the streams, 1.5 us more).
+  static constexpr int NST = D == 256 ? 1 : 2;
+  static constexpr int HALVES = D == 64 ? 1 : 2;  // warpgroups that share a stream's keys
+  static constexpr int SWARPS = 4 * HALVES;       // softmax warps per stream
   static constexpr int CTAS = D == 64 ? 2 : 1;  // per SM
   static constexpr int NQ = KSPLIT ? 1 : NST;  // query tiles held
-  static constexpr int KST = D == 256 ? 1 : 2;  // K stages
+  static constexpr int KST = D == 256 ? 1 : (D == 64 ? 4 : 2);  // K stages
   static constexpr int VST = KST;                                // V stages
   // Producer warps: a warp gets a TMA box out about every 90 cycles (one lane
   // each; 180 from a single lane), so one warp with all 32 boxes of a K and a V
@@ -57,25 +64,43 @@ struct RowsTiling {
   // NKP warps that share a tile's column blocks; V has one, whose boxes span all
   // column blocks (V's tile may lie block by block: see dV; K's has to be whole
   // columns of 128 rows).
-  // Two CTAs on an SM have one warp each for both operands (their registers).
-  static constexpr int NKP = D == 64 ? 1 : 2, NPROD = D == 64 ? 1 : NKP + 1;
+  // (At head size 64, one warp for both operands' boxes held a pair of 64-key steps
+  // at 1.65 us in blocks of 16, 2.2 in blocks of 8; two warps 1.3.)
+  static constexpr int NKP = D == 64 ? 1 : 2, NPROD = NKP + 1;
   static constexpr int COLB = D / 64;
-  static constexpr int CB_BYTES = 128 * 128;  // one column block of 128 rows
+  static constexpr int CB_BYTES = 128 * 128;  // one column block of 128 rows (D = 64 has one)
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
   static constexpr int OFF_K = NQ * Q_BYTES;
   static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
   static constexpr int OFF_XCH = OFF_V + VST * KV_BYTES;
-  static constexpr int XCH_BYTES = NST * 2 * 2 * BM * 4;  // [stream][phase parity][half][row]
+  // [stream][phase parity][half][row]
+  static constexpr int XCH_BYTES = HALVES == 2 ? NST * 2 * 2 * BM * 4 : 0;
   static constexpr int OFF_BAR = OFF_XCH + XCH_BYTES;
   static constexpr int SMEM = 1024 + OFF_BAR + 256;
-  static constexpr int THREADS = NST * 256 + NPROD * 32 + 32;
+  static constexpr int STHREADS = NST * SWARPS * 32;  // softmax threads
+  // Two CTAs of 11 warps would leave 88 registers per thread, and the softmax warps
+  // spilled some of their rows: at head size 64 the CTA is launched with an idle
+  // twelfth warp, and its third warpgroup passes registers to the first two.
+  static constexpr bool PASS_REGS = D == 64;
+  static constexpr int THREADS = STHREADS + NPROD * 32 + (PASS_REGS ? 64 : 32);
+  static constexpr int LAUNCH_REGS = 80, SOFTMAX_REGS = 96, OTHER_REGS = 48;  // (PASS_REGS)
+  static_assert(!PASS_REGS || (STHREADS * SOFTMAX_REGS + (THREADS - STHREADS) * OTHER_REGS <=
+                                   THREADS * LAUNCH_REGS &&
+                               THREADS - STHREADS == 128 &&
+                               CTAS * THREADS * LAUNCH_REGS <= 65536),
+                "registers");
   static constexpr uint32_t TMEM_COLS = 512 / CTAS;
+  // a stream's tensor memory: scores, then weights, in the first BN columns, output
+  // in the next D
+  static constexpr uint32_t TST = TMEM_COLS / NST;
   // an SM holds CTAS of these, no more: their tensor memory is what there is
   static_assert((CTAS + 1) * SMEM > 232448, "CTAs per SM");
-  static_assert(CTAS * SMEM <= 232448 && 128 + D <= TMEM_COLS / NST, "CTAs per SM");
+  static_assert(CTAS * SMEM <= 232448 && BN + D <= TST, "CTAs per SM");
   static_assert(!KSPLIT || NST == 2, "two streams share the keys");
-  static_assert(!KSPLIT || (D * 128 * 4 <= KST * KV_BYTES && 65536 <= VST * KV_BYTES),
+  static_assert(!KSPLIT || (D * 128 * 4 <= KST * KV_BYTES && SWARPS * 4096 <= Q_BYTES &&
+                            SWARPS * 4096 <= VST * KV_BYTES / 2 &&
+                            4 * 128 * 4 <= VST * KV_BYTES / 2),
                 "the join's exchange fits the rings");
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
@@ -210,7 +235,8 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
                 const __grid_constant__ CUtensorMap tmv) {
   constexpr bool LO = std::is_same<T, __nv_bfloat16>::value;
   using Tl = RowsTiling<D, KSPLIT>;
-  constexpr int NST = Tl::NST, BN = Tl::BN;
+  constexpr int NST = Tl::NST, BN = Tl::BN, HALVES = Tl::HALVES;
+  constexpr uint32_t TST = Tl::TST;
 
   grid_dependents_launch();  // what follows on the stream may be scheduled early
   const int G = p.H / p.Hkv;
@@ -283,18 +309,11 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
   const int t_end = static_cast<int>(min(t_beg64 + p.P, static_cast<int64_t>(L)));
   const int NK = (t_end - t_beg + BN - 1) / BN;  // key tiles of the CTA
   // key tiles each stream takes, and its query tokens' rows
-  int nk[NST], nrow[NST];
-#pragma unroll
-  for (int t = 0; t < NST; ++t) {
-    if constexpr (KSPLIT) {
-      nk[t] = (NK + 1 - t) >> 1;
-      nrow[t] = ntok * G;
-    } else {
-      nrow[t] = max(0, min(qpt, ntok - t * qpt)) * G;
-      nk[t] = nrow[t] > 0 ? NK : 0;
-    }
-  }
-  const int nq = KSPLIT ? 1 : (nrow[NST - 1] > 0 ? NST : 1);  // query tiles holding rows
+  auto rows_of = [&](int t) {
+    return (KSPLIT ? ntok : max(0, min(qpt, ntok - t * qpt))) * G;
+  };
+  auto tiles_of = [&](int t) { return KSPLIT ? (NK + 1 - t) >> 1 : (rows_of(t) > 0 ? NK : 0); };
+  const int nq = KSPLIT ? 1 : (rows_of(NST - 1) > 0 ? NST : 1);  // query tiles holding rows
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(
@@ -318,7 +337,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   static_assert((1 + 2 * Tl::KST + 2 * Tl::VST + 4 * NST + 1) * 8 + 8 <= 256, "barriers");
 
-  constexpr int NKP = Tl::NKP, kProducer = 8 * NST, kIssuer = kProducer + Tl::NPROD;
+  constexpr int NKP = Tl::NKP, kProducer = Tl::SWARPS * NST, kIssuer = kProducer + Tl::NPROD;
   const bool producer = warp >= kProducer && warp < kIssuer;
   const int bpt = BN / S;  // cache blocks per key tile
   const int blk0 = t_beg / S, nblk = (t_end + S - 1) / S;
@@ -370,8 +389,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
   // The producers issue Q and the first tiles before the CTA-wide sync, under the
   // tensor-memory allocation.
   static_assert(Tl::KST == Tl::VST, "the first tiles");
-  constexpr bool one_warp = Tl::NPROD == 1;    // for both operands
-  const bool is_v = warp == kProducer + NKP;   // (not one_warp)
+  const bool is_v = warp == kProducer + NKP;
   const int ahead = min(NK, Tl::KST);
   int next_id = -1;
   if (producer) {
@@ -385,9 +403,9 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
       }
       for (int t = 0; t < NST; ++t) {
         mbar_init(&s_full[t], 1);
-        mbar_init(&p_full[t], 8);  // one arrival per softmax warp
+        mbar_init(&p_full[t], Tl::SWARPS);  // one arrival per softmax warp
         mbar_init(&o_done[t], 1);
-        mbar_init(&xch_bar[t], 8);
+        mbar_init(&xch_bar[t], Tl::SWARPS);
       }
       mbar_init(mma_done, 1);
       *abort_flag = 0;
@@ -405,8 +423,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
     }
     __syncwarp();
     for (int j = 0; j < ahead; ++j) {
-      if (one_warp || !is_v) load_tile(false, j, next_id);
-      if (one_warp || is_v) load_tile(true, j, next_id);
+      load_tile(is_v, j, next_id);
       if (j + 1 < NK) next_id = block_id(j + 1);
     }
   }
@@ -419,34 +436,29 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  auto give_regs = [] {
+    if constexpr (Tl::PASS_REGS)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Tl::OTHER_REGS));
+  };
   if (producer) {
+    give_regs();
     // ---------------- producers: the rest of their operand's tiles ----------------
-    int k_issued = ahead, v_issued = ahead;
+    int issued = ahead;
     for (int j = ahead; j < NK; ++j) {
-      if (one_warp || !is_v) {
-        if (!stage_free(false, j)) break;
-        load_tile(false, j, next_id);
-        k_issued = j + 1;
-      }
-      if (one_warp || is_v) {
-        if (!stage_free(true, j)) break;
-        load_tile(true, j, next_id);
-        v_issued = j + 1;
-      }
+      if (!stage_free(is_v, j)) break;
+      load_tile(is_v, j, next_id);
+      issued = j + 1;
       if (j + 1 < NK) next_id = block_id(j + 1);
     }
     // copies in flight land before the CTA can exit
     if (lane == 0) {
       mbar_wait_bounded(q_full, 0);
-      if (one_warp || !is_v)
-        for (int j = max(k_issued - Tl::KST, 0); j < k_issued; ++j)
-          mbar_wait_bounded(&k_full[j % Tl::KST], (j / Tl::KST) & 1);
-      if (one_warp || is_v)
-        for (int j = max(v_issued - Tl::VST, 0); j < v_issued; ++j)
-          mbar_wait_bounded(&v_full[j % Tl::VST], (j / Tl::VST) & 1);
+      for (int j = max(issued - Tl::KST, 0); j < issued; ++j)
+        mbar_wait_bounded(&(is_v ? v_full : k_full)[j % Tl::KST], (j / Tl::KST) & 1);
     }
     __syncwarp();
   } else if (warp == kIssuer) {
+    give_regs();
     // ---------------- MMA issuer (one elected lane), V tail zeroing (whole warp) ----------------
     constexpr int fmt = LO ? 1 : 0;
     constexpr uint32_t idesc_s = tc::instr_desc_f16(fmt, 0, 0, Tl::BM, BN);
@@ -468,13 +480,13 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
         const uint32_t off = ((s >> 2) * Tl::CB_BYTES + (s & 3) * 32) >> 4;
-        mma_ss_on(on, tmem + t * 256, qd + off, kd + off, idesc_s, s > 0);
+        mma_ss_on(on, tmem + t * TST, qd + off, kd + off, idesc_s, s > 0);
       }
       commit_on(on, &s_full[t]);
     };
     auto issue_pv = [&](int t, int st, uint32_t accumulate) {  // O_t += P_t V
       const uint64_t vd = dV + st * (Tl::KV_BYTES >> 4);
-      const uint32_t tS = tmem + t * 256, tO = tS + 128;
+      const uint32_t tS = tmem + t * TST, tO = tS + BN;
 #pragma unroll
       for (int s = 0; s < BN / 16; ++s) {
         const uint64_t bdesc =
@@ -558,20 +570,24 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
     commit_on(on, mma_done);
     mbar_wait_bounded(mma_done, 0);
     __syncwarp();
-  } else {
-    // ---------------- softmax: warps 8t .. 8t + 7 serve stream t; warpgroup half
-    // hw of them takes keys 64 hw .. 64 hw + 63 of each key tile and output
-    // columns hw D / 2 .. of each row; thread r of a warpgroup owns row r ----------------
-    constexpr int HK = BN / 2;  // keys per half
-    constexpr int HD = D / 2;   // output columns per half
-    const int t = warp >> 3;
-    const int hw = (warp >> 2) & 1;
+  } else if (warp < kProducer) {
+    if constexpr (Tl::PASS_REGS)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Tl::SOFTMAX_REGS));
+    // ---------------- softmax: SWARPS warps serve a stream; where they are two
+    // warpgroups, half hw of them takes keys 64 hw .. 64 hw + 63 of each key tile and
+    // output columns hw D / 2 .. of each row; thread r of a warpgroup owns row r ----------------
+    constexpr int HK = BN / HALVES;  // keys per half
+    constexpr int HD = D / HALVES;   // output columns per half
+    static_assert(HK == 64, "scores per thread");
+    const int t = warp / Tl::SWARPS;
+    const int hw = (warp >> 2) & (HALVES - 1);
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tT = tmem + t * 256 + lane_base;
-    const uint32_t tS = tT + hw * HK, tO = tT + 128 + hw * HD;
-    const bool row_on = r < nrow[t];
-    const bool warp_on = (warp & 3) * 32 < nrow[t];  // a warp without rows only keeps step
+    const uint32_t tT = tmem + t * TST + lane_base;
+    const uint32_t tS = tT + hw * HK, tO = tT + BN + hw * HD;
+    const int nrow = rows_of(t);
+    const bool row_on = r < nrow;
+    const bool warp_on = (warp & 3) * 32 < nrow;  // a warp without rows only keeps step
     const int rtok = r / G;
     const int tok = q0 + tok0 + (KSPLIT ? 0 : t * qpt) + rtok;  // this row's query token
     const int head = hk * G + (r - rtok * G);
@@ -579,16 +595,18 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
     if (p.shared_lens && row_on)
       lim = min(lim, shared_part(p.shared_lens[tok], p.lens[tok], p.L_cap, S));
     float m = -INFINITY, l = 0.f;  // l: this half's share of the running sum
-    bool ok = nk[t] > 0;
-    const int nkt = nk[t];
+    const int nkt = tiles_of(t);
+    bool ok = nkt > 0;
     auto slot = [&](int j, int half) { return xch + ((t * 2 + (j & 1)) * 2 + half) * Tl::BM; };
     for (int j = 0; ok && j < nkt; ++j) {
       ok = wait_warp(&s_full[t], j & 1, abort_flag);
       if (!ok) break;
       if (!warp_on) {  // (one arrival per phase: it waits for the phase it arrived at)
-        arrive_warp(&xch_bar[t], lane);
-        ok = wait_warp(&xch_bar[t], j & 1, abort_flag);
-        if (!ok) break;
+        if constexpr (HALVES == 2) {
+          arrive_warp(&xch_bar[t], lane);
+          ok = wait_warp(&xch_bar[t], j & 1, abort_flag);
+          if (!ok) break;
+        }
         arrive_warp(&p_full[t], lane);
         continue;
       }
@@ -612,13 +630,17 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
 #pragma unroll
       for (int c = 0; c < HK; c += 2) mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], x[c], x[c + 1]);
       const float hmax = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-      // the row's max over both halves (slots alternate with the key tile, so a
-      // half never overwrites a value the other has not read yet)
-      slot(j, hw)[r] = hmax;
-      arrive_warp(&xch_bar[t], lane);
-      ok = wait_warp(&xch_bar[t], j & 1, abort_flag);
-      if (!ok) break;
-      const float tmax = fmaxf(hmax, slot(j, hw ^ 1)[r]) * p.scale_log2;
+      float rmax = hmax;
+      if constexpr (HALVES == 2) {
+        // the row's max over both halves (slots alternate with the key tile, so a
+        // half never overwrites a value the other has not read yet)
+        slot(j, hw)[r] = hmax;
+        arrive_warp(&xch_bar[t], lane);
+        ok = wait_warp(&xch_bar[t], j & 1, abort_flag);
+        if (!ok) break;
+        rmax = fmaxf(hmax, slot(j, hw ^ 1)[r]);
+      }
+      const float tmax = rmax * p.scale_log2;
       // The reference max only moves when the tile max exceeds it by more than
       // 2^8 in weight; the weights stay <= 256, exact in the final ratio.
       const float m_new = fmaxf(m, tmax);
@@ -673,13 +695,14 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
       tc::fence_before_sync();
       arrive_warp(&p_full[t], lane);
     }
-    // the row's sum over both halves
-    if (ok) {
-      slot(nkt, hw)[r] = l;
-      arrive_warp(&xch_bar[t], lane);
-      ok = wait_warp(&xch_bar[t], nkt & 1, abort_flag);
+    if constexpr (HALVES == 2) {  // the row's sum over both halves
+      if (ok) {
+        slot(nkt, hw)[r] = l;
+        arrive_warp(&xch_bar[t], lane);
+        ok = wait_warp(&xch_bar[t], nkt & 1, abort_flag);
+      }
+      if (ok) l += slot(nkt, hw ^ 1)[r];
     }
-    if (ok) l += slot(nkt, hw ^ 1)[r];
     if (ok) ok = wait_warp(&o_done[t], 0, abort_flag);
     // The output columns this warp finishes, and its weights: of this stream's
     // result and (KSPLIT) of the other's. Joining, stream t finishes the t-th half
@@ -690,14 +713,16 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
     float w0 = 1.f, w1 = 0.f;
     // 4 KB for its output on the way out: of the stream's query tile, or, of a
     // single stream, of the K ring
-    uint8_t* buf = (NST == 1 ? sK : sQ + (KSPLIT ? 0 : t) * Tl::Q_BYTES) + (warp & 7) * 4096;
-    static_assert(NST == 1 ? Tl::KST * Tl::KV_BYTES >= 32768 : Tl::Q_BYTES >= 32768, "8 warps");
+    const int sw = warp & (Tl::SWARPS - 1);  // of the stream's warps
+    uint8_t* buf = (NST == 1 ? sK : sQ + (KSPLIT ? 0 : t) * Tl::Q_BYTES) + sw * 4096;
+    static_assert(NST == 1 ? Tl::KST * Tl::KV_BYTES >= 32768 : Tl::Q_BYTES >= Tl::SWARPS * 4096,
+                  "the warps' buffers");
     float* jO = reinterpret_cast<float*>(sK);   // [D][128] the columns left, by column
     float* jml = reinterpret_cast<float*>(sV);  // [stream][2][128] m and l
     bool join = false;
     if constexpr (KSPLIT) {
-      if (t == 1) buf = sV + 32768 + (warp & 7) * 4096;
-      join = nk[1] > 0;
+      if (t == 1) buf = sV + Tl::VST * Tl::KV_BYTES / 2 + sw * 4096;
+      join = NK > 1;
       // The rings' memory is free once both streams' MMAs are done with it.
       if (join && ok) ok = wait_warp(&o_done[t ^ 1], 0, abort_flag);
       if (join && ok && warp_on) {
@@ -706,7 +731,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
 #pragma unroll 1
         for (int c0 = 0; c0 < FC; c0 += CH) {
           uint32_t u[CH];
-          tmem_ld_cols(tT + 128 + left + c0, u);
+          tmem_ld_cols(tT + BN + left + c0, u);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < CH; ++c) jO[(left + c0 + c) * 128 + r] = __uint_as_float(u[c]);
@@ -716,7 +741,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
           jml[t * 256 + 128 + r] = l;
         }
       }
-      asm volatile("bar.sync 1, 512;" ::: "memory");  // every softmax thread, aborted or not
+      asm volatile("bar.sync 1, %0;" ::"n"(Tl::STHREADS) : "memory");  // every softmax thread, aborted or not
       if (join && ok) {
         const float mo = jml[(t ^ 1) * 256 + r], lo = jml[(t ^ 1) * 256 + 128 + r];
         const float M = fmaxf(m, mo);
@@ -732,7 +757,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
       const int64_t ih = static_cast<int64_t>(tok) * p.H + head;
       const float inv = direct ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
       const float f0 = w0 * inv, f1 = w1 * inv;
-      const int rows = nrow[t] - (warp & 3) * 32;  // this warp's
+      const int rows = nrow - (warp & 3) * 32;  // this warp's
       const int n_cols = KSPLIT && !join ? HD : FC;
       void* dst = direct ? p.out : static_cast<void*>(p.ws_acc);
       const pa_dtype dst_dt = direct ? p.out_dt : PA_F32;
@@ -740,7 +765,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
 #pragma unroll 1
       for (int c0 = 0; c0 < n_cols; c0 += CH) {
         uint32_t u[CH];
-        tmem_ld_cols(tT + 128 + col0 + c0, u);
+        tmem_ld_cols(tT + BN + col0 + c0, u);
         tc::tmem_wait_ld();
         float v[CH];
 #pragma unroll
@@ -756,6 +781,8 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
         p.ws_l[ih * p.NP + part] = l;
       }
     }
+  } else {
+    give_regs();
   }
   tc::fence_before_sync();
   __syncthreads();
