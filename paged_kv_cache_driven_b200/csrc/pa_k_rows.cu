@@ -2,6 +2,7 @@
 // packed query rows over whole paged key ranges (rows_kernel), the merge of
 // pa_cross's partitions, and their launchers.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "pa_launch.h"
@@ -12,7 +13,7 @@ namespace host {
 namespace {
 
 template <typename T, int D, bool KSPLIT>
-pa_status launch(const RowsParams& prm, const void* q, cudaStream_t stream) {
+pa_status launch(RowsParams prm, const void* q, cudaStream_t stream) {
   using Tl = RowsTiling<D, KSPLIT>;
   auto kern = rows_kernel<T, D, KSPLIT>;
   static bool configured[kMaxDevices] = {};
@@ -29,11 +30,13 @@ pa_status launch(const RowsParams& prm, const void* q, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(prm.NB) * prm.Hkv * prm.S;
   CUtensorMap tmq, tmk, tmv;
   if (!query_rows_map(&tmq, q, prm.T, prm.H, D, prm.H / prm.Hkv, prm.qpt, dt) ||
-      !row_map_now(&tmk, prm.k_cache, rows, D, prm.S, dt) ||
-      !row_cols_map(&tmv, prm.v_cache, rows, D, prm.S, dt))
+      !row_map_now(&tmk, prm.k_cache, rows, D, std::min(prm.S, Tl::BN), dt) ||
+      !row_cols_map(&tmv, prm.v_cache, rows, D, std::min(prm.S, Tl::BN), dt))
     return PA_ERR_CUDA;
   const int64_t groups = ceil_div(prm.max_rows, Tl::NQ * prm.qpt);
   const dim3 grid(static_cast<unsigned>(groups * prm.Hkv), prm.parts, prm.items);
+  prm.longest_first = !prm.shared_lens && prm.items > 1 && prm.items <= 32 &&
+                      static_cast<int64_t>(grid.x) * grid.y * grid.z > Tl::CTAS * sm_count();
   kern<<<grid, Tl::THREADS, Tl::SMEM, stream>>>(prm, tmq, tmk, tmv);
   return cuda_status();
 }

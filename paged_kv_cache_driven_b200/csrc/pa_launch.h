@@ -101,6 +101,7 @@ struct RowsParams {
   int parts;                    // partitions in the grid
   int NP;                       // result slots per (row, head) in the workspace
   int qpt;                      // query rows (tokens) per 128-row tile: 128 / (H / Hkv)
+  bool longest_first;           // (set at launch) items in descending order of length
   pa_dtype out_dt;
 };
 

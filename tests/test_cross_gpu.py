@@ -71,6 +71,27 @@ def test_block_sizes(S):
     check([1, 1], [90, 1200], 2, 2, 64, S, torch.float16)
 
 
+@pytest.mark.parametrize("S", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("D", [64, 256])
+def test_block_sizes_many_rows(D, S):
+    """Blocks shorter and longer than a key tile under whole row tiles, keys split and not."""
+    for partition in (-1, 128):
+        check([40, 200], [777, 130], 2, 2, D, S, torch.bfloat16, partition=partition)
+    check([129, 17, 50], [64, 63, 193], 2, 1, D, S, torch.float16)
+
+
+@pytest.mark.parametrize("B", [2, 7, 32, 33])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_more_than_a_wave_of_uneven_requests(D, B):
+    """Lengths in an order of their own, with equal ones, none, and requests without queries,
+    on more CTAs than run at once (up to 32 requests then start in descending order of length)."""
+    kv = [(0, 130, 64, 400, 130, 1, 257)[(3 * i + 1) % 7] for i in range(B)]
+    q = [(150, 17, 0, 129, 20)[i % 5] for i in range(B)]
+    H = 12 if B > 2 else 160
+    check(q, kv, H, H, D, 16, torch.bfloat16)
+    check(q, [130] * B, H, H, D, 16, torch.float16)
+
+
 @pytest.mark.parametrize("G", [1, 2, 5, 8, 16, 100, 128])
 @pytest.mark.parametrize("q", [1, 3, 60, 300])
 def test_grouped_heads(G, q):
