@@ -17,7 +17,7 @@
 //     S^T = K Q^T (K by ldmatrix, Q^T kept in registers or in a shared tile),
 //     the online softmax per head column (base 2), P^T into the B-operand
 //     layout by movmatrix, O^T += V^T P^T (V^T by ldmatrix.trans), P as a
-//     16-bit hi + lo pair for bf16; masked tokens are removed by selection in
+//     16-bit hi + lo pair (pa_decode_gqa in fp16: hi alone); masked tokens are removed by selection in
 //     the scores and by zeroing their V^T columns;
 //   * the consumers' (m, l, O) merge through shared memory at the end; a
 //     single-partition request writes its output, otherwise the partials go to
@@ -229,6 +229,10 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
   int width = p.MB;  // entries of the table row from trow on
   constexpr bool TAIL = std::is_same<Prm, DecodeParamsTail>::value;
   constexpr bool FAST = FEW || TAIL;
+  // P as a 16-bit value and its rounding residue (see below), and for fp16 times
+  // 2^15: its smallest step, 2^-24, then lies at 2^-39 of the largest weight
+  constexpr bool LO = FAST || std::is_same<TM, __nv_bfloat16>::value;
+  constexpr float SHIFT = FAST && std::is_same<TM, __half>::value ? 15.f : 0.f;
   int ids_a = -1, ids_b = -1;
   auto load_ids = [&](int blk1) {
     const int lim = min(blk1, width);
@@ -671,8 +675,8 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
           const float mr = mn == -INFINITY ? 0.f : mn;
           al[nt][c] = approx_exp2(m[nt][c] - mr);
           any_rescale |= m[nt][c] < mn;
-          pr[c] = approx_exp2(sc[c] - mr);
-          pr[c + 2] = approx_exp2(sc[c + 2] - mr);
+          pr[c] = approx_exp2(sc[c] - (mr - SHIFT));
+          pr[c + 2] = approx_exp2(sc[c + 2] - (mr - SHIFT));
         } else {
           al[nt][c] = mn == -INFINITY ? 1.f : exp2f(m[nt][c] - mn);
           any_rescale |= al[nt][c] != 1.f;
@@ -684,12 +688,14 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
       }
       // P^T as the B operand: tokens 2t, 2t + 1 (b0) and 2t + 8, 2t + 9 (b1) of
       // head g, by transposing the accumulator-layout pairs. bf16 keeps 8 bits,
-      // so P goes in as a hi + lo pair (its rounding drops from 2^-9 to 2^-17);
-      // fp16 keeps 11, within the tolerance on its own.
+      // so P goes in as a hi + lo pair (its rounding drops from 2^-8 to 2^-16).
+      // fp16 keeps 11: as much as the rounding of an fp16 output, so the rows of
+      // pa_cross and pa_decode_shared, which one-head decode works with 32-bit
+      // weights, take a pair too (2^-22); pa_decode_gqa's go in as one term.
       const uint32_t h0 = pack2<TM>(pr[0], pr[1]), h1 = pack2<TM>(pr[2], pr[3]);
       bhi[nt][0] = movmatrix_trans(h0);
       bhi[nt][1] = movmatrix_trans(h1);
-      if (std::is_same<TM, __nv_bfloat16>::value) {
+      if (LO) {
         const float2 f0 = unpack2<TM>(h0), f1 = unpack2<TM>(h1);
         blo[nt][0] = movmatrix_trans(pack2<TM>(pr[0] - f0.x, pr[1] - f0.y));
         blo[nt][1] = movmatrix_trans(pack2<TM>(pr[2] - f1.x, pr[3] - f1.y));
@@ -727,7 +733,7 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
 #pragma unroll
       for (int nt = 0; nt < NHT; ++nt) {
         mma16816<TM>(o[mt][nt], a, bhi[nt][0], bhi[nt][1]);
-        if (std::is_same<TM, __nv_bfloat16>::value)
+        if (LO)
           mma16816<TM>(o[mt][nt], a, blo[nt][0], blo[nt][1]);
       }
     }
@@ -798,7 +804,7 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
       }
     }
     if (!direct && lane == 0) {
-      p.ws_m[wslot] = M;
+      p.ws_m[wslot] = M - SHIFT;  // of the weights that l and O were summed with
       p.ws_l[wslot] = lsum;
     }
   }

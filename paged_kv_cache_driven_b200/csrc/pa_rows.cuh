@@ -25,8 +25,10 @@
 //                   rate at which HBM delivers the keys.
 // Few CTAs are multiplied by partitions of the keys, whose results (m, l, O) a
 // merge kernel joins. Scores, softmax statistics and output accumulate in fp32;
-// the weights enter the second product as two bf16 terms (value and rounding
-// residue) for bf16, as one f16 term for f16.
+// the weights enter the second product as two 16-bit terms, value and rounding
+// residue: 2^-16 of a weight for bf16, 2^-22 for f16 (see kWeightShift for small
+// weights). One f16 term would leave 2^-11 of a weight, as much as an fp16 output's
+// own rounding.
 //
 // Every wait is bounded (about a second); a timeout sets PA_DEVERR_TIMEOUT, stops
 // all roles, waits for the copies and MMAs in flight and frees tensor memory.
@@ -228,12 +230,18 @@ __device__ __forceinline__ void store_out(uint8_t* buf, const float (&v)[C], voi
   }
 }
 
+// f16 weights are held as 2^shift times what they are (the sum l alike, so the
+// ratio stays): f16 ends at 2^-24, and a weight is at most 2^8 (the reference
+// maximum may lag by that much), so the steps of the smallest weights lie at
+// 2^-31 of the largest instead of 2^-24.
+template <typename T>
+constexpr float kWeightShift = std::is_same<T, __half>::value ? 7.f : 0.f;
+
 template <typename T, int D, bool KSPLIT>
 __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, KSPLIT>::CTAS)
     rows_kernel(const RowsParams p, const __grid_constant__ CUtensorMap tmq,
                 const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv) {
-  constexpr bool LO = std::is_same<T, __nv_bfloat16>::value;
   using Tl = RowsTiling<D, KSPLIT>;
   constexpr int NST = Tl::NST, BN = Tl::BN, HALVES = Tl::HALVES;
   constexpr uint32_t TST = Tl::TST;
@@ -486,7 +494,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
   } else if (warp == kIssuer) {
     give_regs();
     // ---------------- MMA issuer (one elected lane), V tail zeroing (whole warp) ----------------
-    constexpr int fmt = LO ? 1 : 0;
+    constexpr int fmt = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
     constexpr uint32_t idesc_s = tc::instr_desc_f16(fmt, 0, 0, Tl::BM, BN);
     constexpr uint32_t idesc_o = tc::instr_desc_f16(fmt, 0, 1, Tl::BM, D);
     const uint32_t on = elect_one();
@@ -519,7 +527,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
             vd + static_cast<uint32_t>((((s >> lg) * Tl::COLB << lg) + (s & ((1 << lg) - 1))) * 128);
         const uint32_t pa = tS + 32 * (s >> 1) + 8 * (s & 1);  // keys 16s .. 16s + 15
         mma_ts_on(on, tO, pa, bdesc, idesc_o, s > 0 ? 1u : accumulate);
-        if constexpr (LO) mma_ts_on(on, tO, pa + 16, bdesc, idesc_o, 1u);
+        mma_ts_on(on, tO, pa + 16, bdesc, idesc_o, 1u);
       }
     };
     auto k_ready = [&](int j) {
@@ -668,17 +676,18 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
       }
       const float tmax = rmax * p.scale_log2;
       // The reference max only moves when the tile max exceeds it by more than
-      // 2^8 in weight; the weights stay <= 256, exact in the final ratio.
+      // 2^8 in weight; the weights stay <= 256 (2^15 with f16's shift), exact in the
+      // final ratio.
       const float m_new = fmaxf(m, tmax);
       const bool grow = m_new > m + 8.f;
       const float m_use = grow ? m_new : m;
       const float alpha = grow ? fast_exp2(m - m_use) : 1.f;
       m = m_use;
       // a row without keys so far keeps m = -inf; its weights are 2^-inf = 0
-      const float m_ref = m_use == -INFINITY ? 0.f : m_use;
+      const float m_ref = (m_use == -INFINITY ? 0.f : m_use) - kWeightShift<T>;
       // P over this half's scores, 8 keys at a time: keys 2k, 2k+1 of a 32-key
-      // chunk q as one 16-bit pair in column 32q + k, and for bf16 the rounding
-      // residue p - bf16(p), itself rounded, in column 32q + 16 + k
+      // chunk q as one 16-bit pair in column 32q + k, and the pair's rounding
+      // residues, themselves rounded, in column 32q + 16 + k
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
       const float2 nm2 = make_float2(-m_ref, -m_ref);
       float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -692,16 +701,12 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
           const float2 pe = make_float2(fast_exp2(tt.x), fast_exp2(tt.y));
           acc[e & 1] = fadd2(acc[e & 1], pe);
           hi[e] = pack_pair<T>(pe.x, pe.y);
-          if constexpr (LO) {
-            // bf16 pair -> the two fp32 values it holds: exact bit moves
-            const float2 hh = make_float2(__uint_as_float(hi[e] << 16),
-                                          __uint_as_float(hi[e] & 0xffff0000u));
-            lo[e] = pack_pair<T>(pe.x - hh.x, pe.y - hh.y);
-          }
+          const float2 hh = Elem<T>::pair(hi[e]);
+          lo[e] = pack_pair<T>(pe.x - hh.x, pe.y - hh.y);
         }
         const uint32_t col = 32 * (g >> 2) + 4 * (g & 3);  // within this half's 64 columns
         tc::tmem_st4(tS + col, hi);
-        if constexpr (LO) tc::tmem_st4(tS + col + 16, lo);
+        tc::tmem_st4(tS + col + 16, lo);
       }
       // The stream's previous product has completed (the commit that released
       // these scores covers it): rescale the rows whose max moved.
@@ -803,7 +808,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
         store_out<CH>(buf, v, dst, dst_dt, row_at + col0 + c0, rows, lane);
       }
       if (!direct && hw == 0 && row_on && (!join || t == 0)) {
-        p.ws_m[ih * p.NP + part] = m;
+        p.ws_m[ih * p.NP + part] = m - kWeightShift<T>;
         p.ws_l[ih * p.NP + part] = l;
       }
     }
