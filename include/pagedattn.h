@@ -440,8 +440,9 @@ pa_status pa_cross(void* out, pa_dtype out_dt, const void* q, const void* k_cach
  * seq_lens[b] == 0 gives an all-zero row; a negative length, a shared length
  * outside [0, max_shared_len] and a group outside [0, B] or of more than
  * max_group requests are flagged PA_DEVERR_SEQ_LEN, with undefined output rows.
- * A request shorter than its group's shared part is exact as long as the V
- * values of the group's shared tokens are finite. D 64, 128 or 256; S 8, 16 or
+ * A request shorter than its group's shared part sees its own tokens only (where
+ * shared tokens behind its end hold infinities or NaN in V, its part is worked
+ * out anew, at about a microsecond per token). D 64, 128 or 256; S 8, 16 or
  * 32; H at most 65535, H / Hkv at most 128; B, NG <= 65534; NB * Hkv * S <= 2^31 - 1; scale finite
  * and > 0; 16-byte aligned q, out, caches and workspace.
  * ------------------------------------------------------------------------- */

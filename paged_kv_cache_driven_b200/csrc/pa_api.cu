@@ -1298,7 +1298,7 @@ pa_status pa_decode_shared(void* out, pa_dtype out_dt, const void* q, const void
     const pa_status rc = pa::host::launch_tails(t, dt, D, S, st);
     if (rc != PA_OK) return rc;
   }
-  return pa::host::launch_shared_merge(t, pl.rows.P, out_dt, D, S, st);
+  return pa::host::launch_shared_merge(t, pl.rows.P, dt, out_dt, D, S, st);
 }
 
 }  // extern "C"

@@ -216,8 +216,8 @@ pa_status launch_few(const DecodeParamsFew& prm, pa_dtype dt, pa_dtype out_dt, i
 pa_status launch_cross_merge(const RowsParams& prm, int D, cudaStream_t stream);
 pa_status launch_tails(const DecodeParamsTail& prm, pa_dtype dt, int D, int S,
                        cudaStream_t stream);                            // pa_k_shared.cu
-pa_status launch_shared_merge(const DecodeParamsTail& prm, int P_shared, pa_dtype out_dt, int D,
-                              int S, cudaStream_t stream);
+pa_status launch_shared_merge(const DecodeParamsTail& prm, int P_shared, pa_dtype dt,
+                              pa_dtype out_dt, int D, int S, cudaStream_t stream);
 
 // Each unit's device error word, read and cleared (ORed into *bits).
 bool take_error_decode16(unsigned int* bits);
