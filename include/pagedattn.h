@@ -440,6 +440,7 @@ pa_status pa_cross(void* out, pa_dtype out_dt, const void* q, const void* k_cach
  * seq_lens[b] == 0 gives an all-zero row; a negative length, a shared length
  * outside [0, max_shared_len] and a group outside [0, B] or of more than
  * max_group requests are flagged PA_DEVERR_SEQ_LEN, with undefined output rows.
+ * (Groups are read where max_shared_len > 0; without it nothing is shared.)
  * A request shorter than its group's shared part sees its own tokens only (where
  * shared tokens behind its end hold infinities or NaN in V, its part is worked
  * out anew, at about a microsecond per token). D 64, 128 or 256; S 8, 16 or

@@ -94,9 +94,13 @@ __global__ void __launch_bounds__(128)
   int L = 0, sh = 0;
   bool cut = false;
   if (live) {  // inputs of the passes before, not their results
-    const int shared = __ldg(p.shared_lens + ih / p.H);
-    L = min(__ldg(p.seq_lens + ih / p.H), p.MB * S);
+    const int shared = __ldg(p.shared_lens + ih / p.H), len = __ldg(p.seq_lens + ih / p.H);
+    L = min(len, p.MB * S);
     sh = shared_part(shared, L, p.shared_cap, S);
+    // (the passes check the same, but a bound of zero leaves its pass out)
+    if (lane == 0 && (len < 0 || len > p.MB * S || L - sh > p.L_cap || shared < 0 ||
+                      shared > p.shared_cap))
+      raise_error(PA_DEVERR_SEQ_LEN);
     cut = sh < shared_part(shared, p.shared_cap, p.shared_cap, S);
   }
   grid_dependency_wait();

@@ -53,3 +53,37 @@ def test_a_short_request_that_sees_a_nan():
     assert torch.equal(out[2].isnan().any(-1), want)
     want[2] = True
     assert torch.equal(out[1].isnan().any(-1), want) and bool(out[1, 2].isnan().all())
+
+
+def test_bounds_of_zero_are_checked_too():
+    """Lengths past a bound of zero, whose pass is then not launched: clamped and flagged."""
+    def flags(b, **bounds):
+        out = b.run(**bounds)
+        torch.cuda.synchronize()
+        return out, binding.pa_get_device_error()
+
+    SEQ = binding.PA_DEVERR_SEQ_LEN
+    b = Batch([(64, [64, 70, 64])], 4, 2, 64, 16, torch.bfloat16)
+    good, err = flags(b)
+    assert err == 0
+    out, err = flags(b, max_tail_len=0)  # request 1's tail is 6 tokens
+    assert err == SEQ and torch.equal(out[[0, 2]], good[[0, 2]])
+    K, V = (tokens(c, b.tables[1], 64) for c in (b.k, b.v))
+    assert_attention(out[1:2], *attention(b.q[1:2], K, V, b.scale), b.dt)
+    # shared lengths beyond a bound of zero: nothing is shared, all of it is tail
+    out, err = flags(b, max_shared_len=0, max_tail_len=70)
+    assert err == SEQ
+    for i, n in enumerate(b.lens):
+        K, V = (tokens(c, b.tables[i], n) for c in (b.k, b.v))
+        assert_attention(out[i:i + 1], *attention(b.q[i:i + 1], K, V, b.scale), b.dt)
+    b.sh.zero_()
+    assert flags(b, max_shared_len=0, max_tail_len=70)[1] == 0
+    out, err = flags(b, max_shared_len=0, max_tail_len=0)
+    assert err == SEQ and bool((out == 0).all())
+    b.seq.copy_(torch.tensor([0, -3, 0]))
+    out, err = flags(b, max_shared_len=0, max_tail_len=0)
+    assert err == SEQ and bool((out == 0).all())
+    b.seq.zero_()
+    assert flags(b, max_shared_len=0, max_tail_len=0)[1] == 0
+    b.sh[2] = -1
+    assert flags(b, max_shared_len=0, max_tail_len=0)[1] == SEQ
