@@ -15,6 +15,7 @@ Usage: python -m paged_kv_cache_driven_b200.build [--verbose] [--force] [--trace
 import concurrent.futures
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -34,6 +35,31 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
          "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
+# Registers per thread that kernels need at launch: unit -> (entry points, at least). Warps that
+# ask for more than the others gave (setmaxnreg) wait for good, so a kernel that the compiler fits
+# into fewer registers than its split counts on (RowsTiling::LAUNCH_REGS) must not be built.
+MIN_REGISTERS = {"pa_k_rows.cu": (r"rows_kernelI\w+Li64ELb1E", 80)}
+
+
+def check_registers(src, log):
+    """Raises where ptxas -v reports fewer registers than MIN_REGISTERS asks of `src`."""
+    rule = MIN_REGISTERS.get(os.path.basename(src))
+    if rule is None:
+        return
+    pattern, least = rule
+    entry, seen = "", 0
+    for line in log.splitlines():
+        m = re.search(r"Compiling entry function '(\w+)'", line)
+        entry = m.group(1) if m else entry
+        m = re.search(r"Used (\d+) registers", line)
+        if m and re.search(pattern, entry):
+            seen += 1
+            if int(m.group(1)) < least:
+                raise RuntimeError(f"{entry}: compiled to {m.group(1)} registers, its register "
+                                   f"split needs {least} at launch")
+    if not seen:
+        raise RuntimeError(f"{os.path.basename(src)}: no register count of {pattern} in ptxas -v")
+
 
 def _obj(src):
     return os.path.join(OBJ, os.path.basename(src) + ".o")
@@ -41,7 +67,7 @@ def _obj(src):
 
 def compile_command(src, verbose=False):
     cmd = [NVCC, *FLAGS, "-c", src, "-o", _obj(src)]
-    if verbose:
+    if verbose or os.path.basename(src) in MIN_REGISTERS:
         cmd[1:1] = ["-Xptxas", "-v"]
     return cmd
 
@@ -79,6 +105,13 @@ def build(force=False, verbose=False):
             if verbose or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
             failed |= r.returncode != 0
+        for src, r in zip(todo, runs):
+            try:
+                if r.returncode == 0:
+                    check_registers(src, r.stdout + r.stderr)
+            except RuntimeError:
+                os.remove(_obj(src))  # (a later build compiles and checks it again)
+                raise
         if failed:
             raise subprocess.CalledProcessError(1, "nvcc")
     if todo or force or stale():

@@ -19,6 +19,7 @@ pa_status launch(RowsParams prm, const void* q, cudaStream_t stream) {
   static bool configured[kMaxDevices] = {};
   if constexpr (Tl::PASS_REGS) {
     // the softmax warps would wait for good for registers the launch did not bring
+    // (the package's build refuses such a kernel, build.py; other builds end here)
     static const int regs = [&] {
       cudaFuncAttributes at = {};
       return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
