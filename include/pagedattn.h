@@ -313,9 +313,13 @@ pa_status pa_decode_gqa(void* out, pa_dtype out_dt, const void* q, const void* k
  *   PA_ROPE_PLAIN   as is
  *   PA_ROPE_LINEAR  f_j / factor
  *   PA_ROPE_NTK     base * factor^(rot_dim / (rot_dim - 2)) in place of base
- *   PA_ROPE_YARN    f_j / factor where a pair makes fewer than `low` turns over
- *                   original_len positions, f_j where it makes more than
- *                   `high`, linear in j between; *amplitude = 0.1 ln(factor) + 1
+ *   PA_ROPE_YARN    f_j up to pair `first`, f_j / factor from pair `last` on, between
+ *                   them the mean of both with weights linear in j. With j(r) =
+ *                   rot_dim ln(original_len / (2 pi r)) / (2 ln base), the pair that
+ *                   makes r turns over original_len positions: first = floor(j(high)),
+ *                   at least 0, last = ceil(j(low)), at most rot_dim - 1 (and
+ *                   first + 0.001 where that is not above first).
+ *                   *amplitude = 0.1 ln(factor) + 1
  *   PA_ROPE_BANDS   f_j / factor where the wavelength 2 pi / f_j exceeds
  *                   original_len / low, f_j where it is below
  *                   original_len / high, linear in original_len / wavelength
