@@ -953,7 +953,7 @@ constexpr int kKeyTile = 128;  // keys per tile of the rows kernel
 
 struct RowsPlan {
   bool few;         // the grouped-query kernel (launch_few), else the rows kernel
-  bool split_keys;  // rows kernel: the CTA's two halves on one row tile
+  bool split_keys;  // rows kernel: the CTA's two streams on one row tile
   int P, parts;     // keys per partition (a multiple of kKeyTile), partitions
 };
 
@@ -1037,7 +1037,7 @@ RowsPlan plan_rows(int items, int max_rows, int G, int Hkv, int D, int max_len, 
       if (!any || cost < best_cost) {
         any = true;
         best_cost = cost;
-        best.split_keys = split != 0;
+        best.split_keys = split != 0 || D == 64;
         best.parts = static_cast<int>(parts);
         best.P = static_cast<int>(per * kKeyTile);
       }

@@ -44,10 +44,10 @@ pa_status launch(RowsParams prm, const void* q, cudaStream_t stream) {
 
 template <typename T>
 pa_status by_size(const RowsParams& prm, const void* q, int D, bool split_keys, cudaStream_t st) {
-  if (D == 64) return launch<T, 64, true>(prm, q, st);
+  if (D == 64 && split_keys) return launch<T, 64, true>(prm, q, st);
   if (D == 128)
     return split_keys ? launch<T, 128, true>(prm, q, st) : launch<T, 128, false>(prm, q, st);
-  if (D == 256) return launch<T, 256, false>(prm, q, st);
+  if (D == 256 && !split_keys) return launch<T, 256, false>(prm, q, st);
   return PA_ERR_INVALID;
 }
 

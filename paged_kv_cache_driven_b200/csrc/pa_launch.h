@@ -206,11 +206,12 @@ pa_status launch_copy_blocks(void* k_cache, void* v_cache, const int32_t* src_ds
 // mode: 0 = keys to k_out, 1 = keys and values to 16-bit caches, 2 = to E4M3 caches
 pa_status launch_rope(const RopeParams& prm, pa_dtype dt, int interleaved, int mode,
                       cudaStream_t stream);                             // pa_k_rope.cu
-// split_keys: the CTA's two halves take alternate key tiles of one row tile
-// (items of at most one row tile), else the same key tiles of two row tiles
+// split_keys: a CTA's two streams take alternate key tiles of one row tile (always
+// at head size 64, never at 256, whose CTA has one stream), else the same key
+// tiles of two row tiles
 pa_status launch_rows(const RowsParams& prm, const void* q, pa_dtype dt, int D, bool split_keys,
                       cudaStream_t stream);                             // pa_k_rows.cu
-// at most 16 rows (tokens x heads of a group) per CTA
+// max_rows tokens x heads of a group: at most 16 rows, one CTA's
 pa_status launch_few(const DecodeParamsFew& prm, pa_dtype dt, pa_dtype out_dt, int D, int S,
                      cudaStream_t stream);                              // pa_k_few.cu
 pa_status launch_cross_merge(const RowsParams& prm, int D, cudaStream_t stream);
