@@ -159,7 +159,7 @@ __device__ __forceinline__ float approx_exp2(float x) {
 // Prm = DecodeParamsFew: few packed query rows over whole key ranges (pa_cross, and
 // the shared part of pa_decode_shared): item i has the query tokens start[i] ..
 // start[i + 1] - 1, and its rows are (token, head of the KV head's group) pairs,
-// row r token r / G, head r % G; the columns of a CTA are up to 16 of them.
+// row r token r / G, head r % G; an item has at most 16 of them, a CTA's columns.
 // With the shared part of a group the keys are those of the longest shared
 // part among the CTA's requests, a column sees those of its own request.
 template <typename T, typename TO, int D, int S, bool APPEND, int NHT, typename TC = T,
@@ -189,9 +189,8 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
       return;
     }
   }
-  int rows = G;        // query rows of this KV head
-  int q0 = 0;          // FEW: the item's first query token
-  int most_rows = G;   // rows that the grid has CTAs for
+  int rows = G;  // query rows of this KV head
+  int q0 = 0;    // FEW: the item's first query token
   if constexpr (FEW) {
     q0 = __ldg(p.start + i);
     const int q1 = __ldg(p.start + i + 1);
@@ -201,20 +200,19 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
       return;
     }
     rows = n * G;
-    most_rows = p.max_rows * G;
+    if (rows == 0) return;
   }
-  const int chunks = (most_rows + 15) / 16;
+  const int chunks = FEW ? 1 : (G + 15) / 16;
   const int hk = blockIdx.y / chunks;
-  const int c0 = (blockIdx.y % chunks) * 16;  // first row (a query head of the group) of this CTA
-  const int gc = min(16, rows - c0);          // rows served here
-  if (FEW && gc <= 0) return;
+  const int c0 = FEW ? 0 : (blockIdx.y % chunks) * 16;  // first query head (of the group) here
+  const int gc = min(16, rows - c0);                    // rows served here
   const int lane = threadIdx.x & 31;
   const int w = threadIdx.x >> 5;
   // a row's place among the rows of q, out and the workspace
   auto row_index = [&](int row) {
     if constexpr (FEW) {
-      const int tok = (c0 + row) / G;
-      return static_cast<int64_t>(q0 + tok) * p.H + hk * G + (c0 + row - tok * G);
+      const int tok = row / G;
+      return static_cast<int64_t>(q0 + tok) * p.H + hk * G + (row - tok * G);
     } else {
       return static_cast<int64_t>(i) * p.H + static_cast<int64_t>(hk) * G + c0 + row;
     }
@@ -247,12 +245,12 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
     if (grouped) {
       // the longest shared part of the requests served here, through that
       // request's table; mostly the first one's, which is asked for meanwhile
-      const int first = q0 + c0 / G;
+      const int first = q0;
       trow = p.block_tables + static_cast<int64_t>(first) * p.MB;
       if (w == NC) load_ids(blk0 + p.P / S);
       int who = first;
       const int tok = first + lane;
-      if (tok <= q0 + (c0 + gc - 1) / G) {
+      if (tok <= q0 + (gc - 1) / G) {
         const int sh = __ldg(p.shared_lens + tok), len = __ldg(p.seq_lens + tok);
         if (w == 0 && part == 0 && hk == 0 && (sh < 0 || sh > p.L_cap || len < 0))
           raise_error(PA_DEVERR_SEQ_LEN);
@@ -567,7 +565,7 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
       for (int nt = 0; nt < NHT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int tok = q0 + (c0 + min(8 * nt + 2 * t + c, gc - 1)) / G;
+          const int tok = q0 + min(8 * nt + 2 * t + c, gc - 1) / G;
           lim[nt][c] = shared_part(__ldg(p.shared_lens + tok), __ldg(p.seq_lens + tok), p.L_cap, S);
           lim_min = min(lim_min, lim[nt][c]);
         }

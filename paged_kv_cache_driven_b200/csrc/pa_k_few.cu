@@ -11,7 +11,7 @@ namespace pa {
 namespace host {
 namespace {
 
-// One CTA per (partition, KV head and chunk of 16 rows, item).
+// One CTA per (partition, KV head, item).
 template <typename T, typename TO, int D, int S, int NHT>
 pa_status launch(const DecodeParamsFew& prm, cudaStream_t stream) {
   using Tg = GqaTiling<D, 2>;
@@ -24,8 +24,7 @@ pa_status launch(const DecodeParamsFew& prm, cudaStream_t stream) {
   if (!row_map_now(&tmk, prm.k_cache, rows, D, S < 16 ? S : 16, dt) ||
       !row_map_now(&tmv, prm.v_cache, rows, D, S < 16 ? S : 16, dt))
     return PA_ERR_CUDA;
-  const int64_t chunks = ceil_div(static_cast<int64_t>(prm.max_rows) * (prm.H / prm.Hkv), 16);
-  const dim3 grid(prm.parts, static_cast<unsigned>(prm.Hkv * chunks), prm.items);
+  const dim3 grid(prm.parts, prm.Hkv, prm.items);
   kern<<<grid, (Tg::NC + 1) * 32, Tg::SMEM, stream>>>(prm, tmk, tmv);
   return cuda_status();
 }
@@ -57,6 +56,8 @@ pa_status by_out(const DecodeParamsFew& prm, pa_dtype out_dt, int D, int S, cuda
 
 pa_status launch_few(const DecodeParamsFew& prm, pa_dtype dt, pa_dtype out_dt, int D, int S,
                      cudaStream_t stream) {
+  // (the plan sends no more here: a CTA's columns are all the rows of its KV head)
+  if (static_cast<int64_t>(prm.max_rows) * (prm.H / prm.Hkv) > 16) return PA_ERR_INVALID;
   return dt == PA_BF16 ? by_out<__nv_bfloat16>(prm, out_dt, D, S, stream)
                        : by_out<__half>(prm, out_dt, D, S, stream);
 }

@@ -46,7 +46,7 @@ struct RowsTiling {
   static constexpr int BM = 128;              // query rows per tile (MMA M)
   static constexpr int BN = D == 64 ? 64 : 128;  // keys per tile
   // Streams: two, or one at head size 256, which fills tensor and shared memory.
-  // At head size 64 two CTAs share an SM (256 tensor-memory columns and some 85 KB
+  // At head size 64 two CTAs share an SM (256 tensor-memory columns and 81 KB
   // each) and cover each other's start and end, and a stream is one warpgroup with
   // tiles of 64 keys, whose threads hold whole rows: four chains of product,
   // softmax, product are then under way on an SM, and none waits for another's
@@ -167,20 +167,6 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) {
-  tc::tmem_ld32(taddr, r);
-}
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
 // Stores 4 W bytes of each of a warp's 32 rows (lane r holds row r's W words; the
 // rows' destinations differ, rows from `rows` on are not stored) through 32 x W
 // words of shared memory, so that every store instruction writes whole
@@ -189,9 +175,10 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) 
 template <int W>
 __device__ __forceinline__ void store_rows(uint8_t* buf, const uint32_t (&w)[W], uint8_t* dst,
                                            int rows, int lane) {
+  static_assert(W == 32 || W == 16, "32 columns in 32 or 16 bits");
   constexpr int NP = W / 4;  // 16-byte pieces per row
   auto place = [](int row, int piece) {
-    const int x = W == 32 ? row & 7 : (W == 16 ? (row >> 1) & 3 : (row >> 2) & 1);
+    const int x = W == 32 ? row & 7 : (row >> 1) & 3;
     return row * W * 4 + ((piece ^ x) << 4);
   };
   __syncwarp();  // the warp's previous use of buf is over
@@ -210,10 +197,10 @@ __device__ __forceinline__ void store_rows(uint8_t* buf, const uint32_t (&w)[W],
   }
 }
 
-// C consecutive output elements of each of a warp's rows, in the output's type.
-template <int C>
-__device__ __forceinline__ void store_out(uint8_t* buf, const float (&v)[C], void* out,
+// 32 consecutive output elements of each of a warp's rows, in the output's type.
+__device__ __forceinline__ void store_out(uint8_t* buf, const float (&v)[32], void* out,
                                           pa_dtype dt, int64_t at, int rows, int lane) {
+  constexpr int C = 32;
   if (dt == PA_F32) {
     uint32_t w[C];
 #pragma unroll
@@ -739,7 +726,8 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
     // result and (KSPLIT) of the other's. Joining, stream t finishes the t-th half
     // of each half's columns, and leaves the others to the other stream.
     constexpr int FC = KSPLIT ? HD / 2 : HD;   // columns to finish
-    constexpr int CH = FC < 32 ? FC : 32;      // columns at a time
+    constexpr int CH = 32;                     // columns at a time
+    static_assert(FC % CH == 0, "whole loads of columns");
     const int col0 = hw * HD + (KSPLIT ? t * FC : 0);
     float w0 = 1.f, w1 = 0.f;
     // 4 KB for its output on the way out: of the stream's query tile, or, of a
@@ -762,7 +750,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
 #pragma unroll 1
         for (int c0 = 0; c0 < FC; c0 += CH) {
           uint32_t u[CH];
-          tmem_ld_cols(tT + BN + left + c0, u);
+          tc::tmem_ld32(tT + BN + left + c0, u);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < CH; ++c) jO[(left + c0 + c) * 128 + r] = __uint_as_float(u[c]);
@@ -796,7 +784,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
 #pragma unroll 1
       for (int c0 = 0; c0 < n_cols; c0 += CH) {
         uint32_t u[CH];
-        tmem_ld_cols(tT + BN + col0 + c0, u);
+        tc::tmem_ld32(tT + BN + col0 + c0, u);
         tc::tmem_wait_ld();
         float v[CH];
 #pragma unroll
@@ -805,7 +793,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
 #pragma unroll
           for (int c = 0; c < CH; ++c) v[c] = fmaf(jO[(col0 + c0 + c) * 128 + r], f1, v[c]);
         }
-        store_out<CH>(buf, v, dst, dst_dt, row_at + col0 + c0, rows, lane);
+        store_out(buf, v, dst, dst_dt, row_at + col0 + c0, rows, lane);
       }
       if (!direct && hw == 0 && row_on && (!join || t == 0)) {
         p.ws_m[ih * p.NP + part] = m - kWeightShift<T>;
