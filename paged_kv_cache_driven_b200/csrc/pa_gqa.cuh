@@ -231,6 +231,7 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
   // 2^15: its smallest step, 2^-24, then lies at 2^-39 of the largest weight
   constexpr bool LO = FAST || std::is_same<TM, __nv_bfloat16>::value;
   constexpr float SHIFT = FAST && std::is_same<TM, __half>::value ? 15.f : 0.f;
+  constexpr float UNSHIFT = SHIFT > 0.f ? 0x1p-15f : 1.f;
   int ids_a = -1, ids_b = -1;
   auto load_ids = [&](int blk1) {
     const int lim = min(blk1, width);
@@ -673,8 +674,8 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
           const float mr = mn == -INFINITY ? 0.f : mn;
           al[nt][c] = approx_exp2(m[nt][c] - mr);
           any_rescale |= m[nt][c] < mn;
-          pr[c] = approx_exp2(sc[c] - (mr - SHIFT));
-          pr[c + 2] = approx_exp2(sc[c + 2] - (mr - SHIFT));
+          pr[c] = approx_exp2((sc[c] - mr) + SHIFT);  // (mr - SHIFT could round)
+          pr[c + 2] = approx_exp2((sc[c + 2] - mr) + SHIFT);
         } else {
           al[nt][c] = mn == -INFINITY ? 1.f : exp2f(m[nt][c] - mn);
           any_rescale |= al[nt][c] != 1.f;
@@ -793,6 +794,9 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
 #pragma unroll
       for (int c = 0; c < NC; ++c) a = fmaf(wt[c], mg[(c * ROWS + row) * (D + 2) + 2 + d], a);
       if constexpr (EB == 1) a *= p.v_scale;
+      if constexpr (SHIFT > 0.f) {
+        if (!direct) a *= UNSHIFT;
+      }
       if (direct) {
         // (FEW: a NaN in q or in a key stays NaN)
         const bool some = FEW ? lsum != 0.f : lsum > 0.f;
@@ -802,8 +806,8 @@ __global__ void __launch_bounds__((GqaTiling<D, sizeof(TC)>::NC + 1) * 32,
       }
     }
     if (!direct && lane == 0) {
-      p.ws_m[wslot] = M - SHIFT;  // of the weights that l and O were summed with
-      p.ws_l[wslot] = lsum;
+      p.ws_m[wslot] = M;
+      p.ws_l[wslot] = lsum * UNSHIFT;
     }
   }
 }

@@ -217,18 +217,17 @@ __device__ __forceinline__ void store_out(uint8_t* buf, const float (&v)[32], vo
   }
 }
 
-// f16 weights are held as 2^shift times what they are (the sum l alike, so the
-// ratio stays): f16 ends at 2^-24, and a weight is at most 2^8 (the reference
-// maximum may lag by that much), so the steps of the smallest weights lie at
-// 2^-31 of the largest instead of 2^-24.
-template <typename T>
-constexpr float kWeightShift = std::is_same<T, __half>::value ? 7.f : 0.f;
+// f16 weights are held as 2^7 times what they are (the sum l alike): f16 ends at
+// 2^-24, and a weight is at most 2^8 (the reference maximum may lag by that much),
+// so the steps of the smallest weights lie at 2^-31 of the largest instead of 2^-24.
+constexpr float kWeightShift = 7.f;
 
 template <typename T, int D, bool KSPLIT>
 __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, KSPLIT>::CTAS)
     rows_kernel(const RowsParams p, const __grid_constant__ CUtensorMap tmq,
                 const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv) {
+  constexpr bool F16 = std::is_same<T, __half>::value;
   using Tl = RowsTiling<D, KSPLIT>;
   constexpr int NST = Tl::NST, BN = Tl::BN, HALVES = Tl::HALVES;
   constexpr uint32_t TST = Tl::TST;
@@ -481,7 +480,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
   } else if (warp == kIssuer) {
     give_regs();
     // ---------------- MMA issuer (one elected lane), V tail zeroing (whole warp) ----------------
-    constexpr int fmt = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+    constexpr int fmt = F16 ? 0 : 1;
     constexpr uint32_t idesc_s = tc::instr_desc_f16(fmt, 0, 0, Tl::BM, BN);
     constexpr uint32_t idesc_o = tc::instr_desc_f16(fmt, 0, 1, Tl::BM, D);
     const uint32_t on = elect_one();
@@ -661,22 +660,26 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
         if (!ok) break;
         rmax = fmaxf(hmax, slot(j, hw ^ 1)[r]);
       }
-      const float tmax = rmax * p.scale_log2;
       // The reference max only moves when the tile max exceeds it by more than
       // 2^8 in weight; the weights stay <= 256 (2^15 with f16's shift), exact in the
-      // final ratio.
-      const float m_new = fmaxf(m, tmax);
-      const bool grow = m_new > m + 8.f;
-      const float m_use = grow ? m_new : m;
-      const float alpha = grow ? fast_exp2(m - m_use) : 1.f;
+      // final ratio. For bf16 it is scale x the score, a score's distance from it
+      // one fused operation, and the weight of a score whose 32-bit steps exceed 1
+      // (2^24 and more) off by up to half a step, which bf16 has the range for and
+      // the ratio cancels. f16 has not, so there m is a score and the distance is
+      // taken before it is scaled.
+      const float top = F16 ? rmax : rmax * p.scale_log2;
+      const bool grow = F16 ? (top - m) * p.scale_log2 > 8.f : top > m + 8.f;  // (from m = -inf too)
+      const float m_use = grow ? top : m;
+      const float alpha = grow ? fast_exp2(F16 ? (m - m_use) * p.scale_log2 : m - m_use) : 1.f;
       m = m_use;
       // a row without keys so far keeps m = -inf; its weights are 2^-inf = 0
-      const float m_ref = (m_use == -INFINITY ? 0.f : m_use) - kWeightShift<T>;
+      const float m_ref = m_use == -INFINITY ? 0.f : m_use;
       // P over this half's scores, 8 keys at a time: keys 2k, 2k+1 of a 32-key
       // chunk q as one 16-bit pair in column 32q + k, and the pair's rounding
       // residues, themselves rounded, in column 32q + 16 + k
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
       const float2 nm2 = make_float2(-m_ref, -m_ref);
+      const float2 shift2 = make_float2(kWeightShift, kWeightShift);
       float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int g = 0; g < HK / 8; ++g) {
@@ -684,7 +687,8 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 tt = ffma2(make_float2(v[2 * e], v[2 * e + 1]), sc2, nm2);
+          const float2 vv = make_float2(v[2 * e], v[2 * e + 1]);
+          const float2 tt = F16 ? ffma2(fadd2(vv, nm2), sc2, shift2) : ffma2(vv, sc2, nm2);
           const float2 pe = make_float2(fast_exp2(tt.x), fast_exp2(tt.y));
           acc[e & 1] = fadd2(acc[e & 1], pe);
           hi[e] = pack_pair<T>(pe.x, pe.y);
@@ -721,6 +725,7 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
       }
       if (ok) l += slot(nkt, hw ^ 1)[r];
     }
+    if constexpr (F16) m *= p.scale_log2;
     if (ok) ok = wait_warp(&o_done[t], 0, abort_flag);
     // The output columns this warp finishes, and its weights: of this stream's
     // result and (KSPLIT) of the other's. Joining, stream t finishes the t-th half
@@ -774,7 +779,8 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
     if (ok && warp_on) {
       tc::fence_after_sync();
       const int64_t ih = static_cast<int64_t>(tok) * p.H + head;
-      const float inv = direct ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+      constexpr float kUnshift = F16 ? 0x1p-7f : 1.f;  // (of partial results)
+      const float inv = direct ? (l != 0.f ? 1.f / l : 0.f) : kUnshift;
       const float f0 = w0 * inv, f1 = w1 * inv;
       const int rows = nrow - (warp & 3) * 32;  // this warp's
       const int n_cols = KSPLIT && !join ? HD : FC;
@@ -796,8 +802,8 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
         store_out(buf, v, dst, dst_dt, row_at + col0 + c0, rows, lane);
       }
       if (!direct && hw == 0 && row_on && (!join || t == 0)) {
-        p.ws_m[ih * p.NP + part] = m - kWeightShift<T>;
-        p.ws_l[ih * p.NP + part] = l;
+        p.ws_m[ih * p.NP + part] = m;
+        p.ws_l[ih * p.NP + part] = l * kUnshift;
       }
     }
   } else {

@@ -105,3 +105,38 @@ def test_shared_prefix(H, Hkv, D, n, dt):
         out = b.run(torch.float32)
         assert binding.pa_get_device_error() == 0
         assert_weights(out, b.q, b.scale, 1, dt)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [1, 40, 200])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_beyond_the_integers(D, rows, dt):
+    """Scores from 2^18 to 2^30, where 32-bit steps exceed what the weights are scaled by: equal scores
+    give V's mean, a larger one takes all."""
+    S, n = 16, 300
+    NB = -(-n // S)
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    v = torch.randn((NB, 4, S, D), generator=g, device=DEV).to(dt)
+    bt = torch.arange(NB, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    start = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    V = v.transpose(1, 2).reshape(NB * S, 4, D)[:n].double()
+    for size in (1000, 3000, 6000, 10000, 14000, 20000, 24000, 28000, 34000, 40000, 60000):
+        q = torch.zeros((rows, 4, D), device=DEV, dtype=dt)
+        q[..., 0] = size
+        for top in (None, 5, 100, 200, 299):
+            k = torch.zeros_like(v)
+            k[..., 0] = size
+            if top is not None:  # a step of the 16-bit types: scores higher by 2^7 and more
+                k[top // S, :, top % S, 0] = size * 1.01
+            for partition in (-1, 128):
+                out = torch.full((rows, 4, D), 7.0, device=DEV)
+                b = binding.pa_cross_workspace_bytes(1, rows, 4, 4, D, rows, n, partition)
+                ws = torch.full((b,), 255, dtype=torch.uint8, device=DEV) if b else None
+                binding.pa_cross(out, q, k, v, bt, lens, start, 0.125, rows, n,
+                                 partition=partition, workspace=ws)
+                want = V.mean(0) if top is None else V[top]
+                off = (out.double() - want).abs().amax()
+                # 32-bit sums of 300 values below 6
+                assert bool(off <= 2.0 ** -15), f"{size} {top} {partition}: {off}"
+    assert binding.pa_get_device_error() == 0
