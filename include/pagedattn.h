@@ -442,8 +442,9 @@ pa_status pa_cross(void* out, pa_dtype out_dt, const void* q, const void* k_cach
  *   workspace     pa_decode_shared_workspace_bytes(...) for the same arguments, as
  *                 in pa_decode
  * seq_lens[b] == 0 gives an all-zero row; a negative length, a shared length
- * outside [0, max_shared_len] and a group outside [0, B] or of more than
- * max_group requests are flagged PA_DEVERR_SEQ_LEN, with undefined output rows.
+ * outside [0, max_shared_len], a group outside [0, B] or of more than max_group
+ * requests and requests outside every group are flagged PA_DEVERR_SEQ_LEN, with
+ * undefined output rows.
  * (Groups are read where max_shared_len > 0; without it nothing is shared.)
  * A request shorter than its group's shared part sees its own tokens only (where
  * shared tokens behind its end hold infinities or NaN in V, its part is worked

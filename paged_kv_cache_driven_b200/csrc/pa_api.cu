@@ -1278,6 +1278,8 @@ pa_status pa_decode_shared(void* out, pa_dtype out_dt, const void* q, const void
   t.block_tables = block_tables;
   t.seq_lens = seq_lens;
   t.shared_lens = shared_lens;
+  t.group_start = group_start;
+  t.NG = NG;
   t.ws_m = ws_m;
   t.ws_l = ws_l;
   t.ws_acc = ws_acc;

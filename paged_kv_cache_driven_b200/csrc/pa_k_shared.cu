@@ -101,6 +101,9 @@ __global__ void __launch_bounds__(128)
     if (lane == 0 && (len < 0 || len > p.MB * S || L - sh > p.L_cap || shared < 0 ||
                       shared > p.shared_cap))
       raise_error(PA_DEVERR_SEQ_LEN);
+    if (ih == 0 && lane == 0 && p.part0 > 0 &&
+        (__ldg(p.group_start) != 0 || __ldg(p.group_start + p.NG) != p.B))
+      raise_error(PA_DEVERR_SEQ_LEN);  // requests outside every group
     cut = sh < shared_part(shared, p.shared_cap, p.shared_cap, S);
   }
   grid_dependency_wait();

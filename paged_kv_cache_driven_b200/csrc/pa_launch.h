@@ -110,6 +110,8 @@ struct RowsParams {
 // slot part0 + partition of the workspace's NP slots.
 struct DecodeParamsTail : DecodeParams {
   const int32_t* shared_lens;  // [B]
+  const int32_t* group_start;  // [NG + 1]
+  int NG;
   int part0;
   int shared_cap;              // host bound on shared_lens
   int tail_parts;              // partitions in the grid

@@ -87,3 +87,17 @@ def test_bounds_of_zero_are_checked_too():
     assert flags(b, max_shared_len=0, max_tail_len=0)[1] == 0
     b.sh[2] = -1
     assert flags(b, max_shared_len=0, max_tail_len=0)[1] == SEQ
+
+
+@pytest.mark.parametrize("n", [2, 30])
+def test_requests_outside_every_group_are_flagged(n):
+    """Groups that do not cover the batch leave requests without their shared part."""
+    b = Batch([(64, [70 + i for i in range(n)]), (32, [40, 50])], 2, 2, 64, 16, torch.bfloat16)
+    good = b.run()
+    assert binding.pa_get_device_error() == 0
+    for starts, kept in (([0, n, n + 1], slice(0, n + 1)), ([1, n, n + 2], slice(1, n + 2)),
+                         ([0, n], slice(0, n))):
+        b.start = torch.tensor(starts, dtype=torch.int32, device=DEV)
+        out = b.run()
+        assert binding.pa_get_device_error() == binding.PA_DEVERR_SEQ_LEN
+        assert torch.equal(out[kept], good[kept])
