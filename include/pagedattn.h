@@ -354,7 +354,9 @@ pa_status pa_rope_table(double* table, int rot_dim, double base, pa_rope_scaling
  * H or Hkv may be 0 (that part's pointers are then not looked at). D a multiple
  * of 8, at most 256; rot_dim even, 2 .. D; strides multiples of 8 elements
  * and at least heads * D; 16-byte aligned q, k, q_out, k_out; table 8-byte
- * aligned. eps finite and >= 0, amplitude finite. T == 0 is a no-op. */
+ * aligned. eps finite and >= 0, amplitude finite. T == 0 is a no-op. (Pairs rot_dim / 2
+ * apart move as single elements where D or rot_dim is no multiple of 16, which takes
+ * about twice the time; interleaved pairs do not.) */
 pa_status pa_rope(void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
                   const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                   const int32_t* positions, const double* table, int rot_dim, int interleaved,
@@ -365,7 +367,7 @@ pa_status pa_rope(void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_
  * v_stride) go to k_cache, v_cache [NB, Hkv, S, D] at slot_mapping as in
  * pa_kv_append (negative slots skip a token's k and v, its q_out is written all
  * the same; slots at or past NB * S are skipped and flagged PA_DEVERR_SLOT;
- * slots must be distinct). v is copied bit for bit. The result is pa_rope's
+ * slots must be distinct). q_out may be q (same stride). v is copied bit for bit. The result is pa_rope's
  * followed by pa_kv_append's, bit for bit, in one pass over the data. Hkv >= 1;
  * H may be 0. Caches 16-byte aligned. */
 pa_status pa_rope_append(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,

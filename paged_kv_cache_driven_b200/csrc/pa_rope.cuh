@@ -33,7 +33,8 @@ namespace pa {
 enum : int {
   kPairs = 0,     // interleaved: elements 2j, 2j + 1; a thread's are consecutive
   kHalf = 1,      // elements j, j + rot / 2: two pieces of EPT / 2 elements, aligned
-  kHalfAny = 2    // the same for any even rot: single elements
+  kHalfAny = 2    // the same for any even rot: single elements (16,384 tokens of 32 + 32
+                  // heads of 96: 174 us with 24 rotated, 86 with all by kHalf)
 };
 enum : int { kNoCache = 0, kCache16 = 1, kCache8 = 2 };
 constexpr int kRopeTokens = 8;  // most tokens of a CTA

@@ -96,3 +96,19 @@ def test_into_a_cache(per_sm, more, D, rot, interleaved, norm, e4m3):
     keep[at] = False
     for r, b in zip(rows, before):
         assert torch.equal(r[keep], b.transpose(1, 2).reshape(NB * S, Hkv, D)[keep])
+
+
+def test_append_with_q_in_place():
+    """q rotated where it lies in the fused projection while k and v go to the cache."""
+    T, H, Hkv, D, S = 75, 6, 2, 128, 16
+    (q, k, v), (qw, kw), pos = inputs(T, H, Hkv, D, torch.bfloat16, True, 1)
+    table = binding.pa_rope_table(D)[0].to(DEV)
+    slots = torch.arange(T, device=DEV)
+    cache = torch.zeros((4, 5, Hkv, S, D), dtype=torch.bfloat16, device=DEV)
+    want = torch.empty_like(q).contiguous()
+    how = dict(q_weight=qw, k_weight=kw)
+    binding.pa_rope_append(want, q, k, v, pos, slots, cache[0], cache[1], table, **how)
+    k0, v0 = k.clone(), v.clone()
+    binding.pa_rope_append(q, q, k, v, pos, slots, cache[2], cache[3], table, **how)
+    assert torch.equal(q, want) and torch.equal(k, k0) and torch.equal(v, v0)
+    assert torch.equal(cache[:2], cache[2:]) and binding.pa_get_device_error() == 0
