@@ -134,8 +134,8 @@ __device__ __forceinline__ float2 unpack2(uint32_t x) {
 
 // CTAs per SM asked of the compiler (0: its choice). Few rows at head size 64 in
 // two column tiles took 112 registers, four CTAs; with five (eight documents of
-// 992 to 4,000 shared tokens, 3 to 16 requests each) 76.2 -> 71.5 us, and no more with
-// six, which spill.
+// 992 to 4,000 shared tokens, 3 to 16 requests each, fp16) 73.7 -> 69.6 us a call,
+// with 8 bytes spilled; six spill more and gain nothing.
 template <typename Prm>
 constexpr int gqa_min_ctas(int D, int NHT) {
   return std::is_same<Prm, DecodeParamsFew>::value && D == 64 && NHT == 2 ? 5 : 0;

@@ -179,8 +179,8 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
 // as nothing leaves the normal range. So x is first cut to +-512 scale, whose
 // codes are those of the limit 448 all the same (NaN stays NaN), and scales lie in
 // [2^-60, 2^60]. (Quotients so small that a remainder is not exact are far below
-// 2^-10, code 0.) 12,289 tokens of 32 heads: 102 us; with a branch to the division
-// for other scales, 109.
+// 2^-10, code 0.) 12,289 tokens of 32 heads: 105 us a call; a branch to the
+// division for other scales took 7 us more.
 struct Quotient {
   float scale, inv, lim;
   __device__ __forceinline__ explicit Quotient(float s)

@@ -50,9 +50,9 @@ struct RowsTiling {
   // each) and cover each other's start and end, and a stream is one warpgroup with
   // tiles of 64 keys, whose threads hold whole rows: four chains of product,
   // softmax, product are then under way on an SM, and none waits for another's
-  // row maximum. 128 rows x 128 keys take 0.95 us of an SM in bf16, 0.80 in f16,
-  // where two chains of two warpgroups each took 1.16 and 0.89 (16 ragged prompts on
-  // 32 heads 117.4 -> 98.7 us; a CTA's end, which joins the streams, 1.5 us more).
+  // row maximum. 128 rows x 128 keys take 0.95 us of an SM in bf16, where two chains
+  // of two warpgroups each took 1.16 (16 ragged prompts on 32 heads, in a captured
+  // graph, 117.4 -> 98.7 us; a CTA's end, which joins the streams, 1.5 us more).
   static constexpr int NST = D == 256 ? 1 : 2;
   static constexpr int HALVES = D == 64 ? 1 : 2;  // warpgroups that share a stream's keys
   static constexpr int SWARPS = 4 * HALVES;       // softmax warps per stream
@@ -251,8 +251,9 @@ __global__ void __launch_bounds__(RowsTiling<D, KSPLIT>::THREADS, RowsTiling<D, 
   // The item, its queries and (pa_cross) its number of keys. Where there is more than
   // a wave of CTAs, those of long items start first, so that the last to end are
   // short ones: the item is then the blockIdx.z-th in descending order of length,
-  // found by each warp from the lengths, one per lane (16 ragged prompts 98.7 ->
-  // 92.3 us on 32 heads of 64, 8 prompts 80.5 -> 61.5 on 16/4 heads of 256).
+  // found by each warp from the lengths, one per lane, so of at most 32 (in a captured
+  // graph: 16 ragged prompts 98.7 -> 92.9 us on 32 heads of 64, 8 prompts 80.5 -> 62
+  // on 16/4 heads of 256).
   int i = blockIdx.z, q0, q1, L = 0;
   if (p.longest_first) {
     const int k = min(lane, p.items - 1);
