@@ -17,8 +17,8 @@
 //     S^T = K Q^T (K by ldmatrix, Q^T kept in registers or in a shared tile),
 //     the online softmax per head column (base 2), P^T into the B-operand
 //     layout by movmatrix, O^T += V^T P^T (V^T by ldmatrix.trans), P as a
-//     16-bit hi + lo pair (pa_decode_gqa in fp16: hi alone); masked tokens are removed by selection in
-//     the scores and by zeroing their V^T columns;
+//     16-bit hi + lo pair (pa_decode_gqa in fp16: hi alone); masked tokens are
+//     removed by selection in the scores and by zeroing their V^T columns;
 //   * the consumers' (m, l, O) merge through shared memory at the end; a
 //     single-partition request writes its output, otherwise the partials go to
 //     the split-KV workspace for splitkv_reduce_kernel.
